@@ -7,7 +7,9 @@ not need the library.
 """
 
 _API = ("absorb_q", "decode_splitkv", "combine", "absorb_out", "decode", "Decoder", "dims_for",
-        "make_dims", "get_device_error", "num_parts_for", "workspace_bytes", "plan")
+        "make_dims", "get_device_error", "num_parts_for", "workspace_bytes", "plan", "step_plan",
+        "rope_frequencies", "rotary", "append_kv_slots", "append_kv_slots_fp8", "decode_tree",
+        "decode_tree_fp8", "tree_attend")
 
 
 def __getattr__(name):

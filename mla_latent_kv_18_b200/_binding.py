@@ -1,4 +1,4 @@
-"""ctypes binding of ``libmla_b200.so`` (the C ABI in include/mla_decode.h).
+"""ctypes binding of ``libmla_b200.so`` (the C ABI in include/mla_decode.h and mla_step.h).
 
 Argument marshalling only: every step runs in the library's CUDA kernels.
 Importing this module loads the library and raises ``ImportError`` if it is
@@ -21,7 +21,10 @@ EXPORTS = ("mla_absorb_q", "mla_decode_num_parts", "mla_decode_workspace_bytes",
            "mla_absorb_q_rope", "mla_prefill_workspace_bytes", "mla_decompress_kv",
            "mla_prefill_attention", "mla_prefill", "mla_append_kv",
            "mla_append_kv_fp8", "mla_gather_dequant_fp8", "mla_decompress_kv_fp8",
-           "mla_default_num_splits", "mla_decode_workspace_size", "mla_decode_splitkv_fp8")
+           "mla_default_num_splits", "mla_decode_workspace_size", "mla_decode_splitkv_fp8",
+           "mla_step_plan", "mla_rope_frequencies", "mla_rotary", "mla_append_kv_slots",
+           "mla_append_kv_slots_fp8", "mla_tree_num_parts", "mla_tree_workspace_bytes",
+           "mla_decode_tree", "mla_decode_tree_fp8")
 
 
 class MLADims(ctypes.Structure):
@@ -33,6 +36,13 @@ class MLADims(ctypes.Structure):
 class MLAPool(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
                 ("token_stride", ctypes.c_int64)]
+
+
+class MLARotaryTensor(ctypes.Structure):
+    # "in" is a keyword: the first field is named src here
+    _fields_ = [("src", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_token", ctypes.c_int64),
+                ("in_head", ctypes.c_int64), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
 
 
 class MLAError(RuntimeError):
@@ -49,6 +59,8 @@ def _load():
     P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     D = ctypes.POINTER(MLADims)
     PL = ctypes.POINTER(MLAPool)
+    RT = ctypes.POINTER(MLARotaryTensor)
+    f32, f64 = ctypes.c_float, ctypes.c_double
     sig = {
         "mla_absorb_q": (i32, [D, P, P, P, P, i32, P]),
         "mla_decode_num_parts": (i32, [D, i64, i32]),
@@ -76,6 +88,16 @@ def _load():
         "mla_default_num_splits": (i32, [D, i32, i32, i32]),
         "mla_decode_workspace_size": (sz, [D, i32, i32]),
         "mla_decode_splitkv_fp8": (i32, [D, P, PL, P, PL, i32, P, i32, P, i32, i32, P, sz, P]),
+        "mla_step_plan": (i32, [P, P, i32, P, i32, P, P, i32, P, i32, i32, P, P, P, P, P, P, P, P]),
+        "mla_rope_frequencies": (i32, [i32, f64, i32, f64, f64, f64, f64, P, P]),
+        "mla_rotary": (i32, [RT, RT, i32, i32, i32, i32, i32, P, P, f32, i32, i32, P]),
+        "mla_append_kv_slots": (i32, [D, P, i64, P, i64, P, P, P, f32, i32, i32, PL, PL, i32, P]),
+        "mla_append_kv_slots_fp8": (i32, [D, P, i64, P, i64, P, P, P, f32, i32, i32, PL, P, PL, i32, P]),
+        "mla_tree_num_parts": (i32, [D, i32]),
+        "mla_tree_workspace_bytes": (sz, [D, i32]),
+        "mla_decode_tree": (i32, [D, P, i32, PL, PL, i32, P, i32, P, P, i32, P, i32, i32, P, sz, P, P, P]),
+        "mla_decode_tree_fp8": (i32, [D, P, i32, PL, P, PL, i32, P, i32, P, P, i32, P, i32, i32, P, sz, P, P,
+                                      P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -10,8 +10,19 @@ every step runs in the library's sm_100a kernels.
 or ``decode(...)`` for all four. A step with many query tokens per sequence
 (``prefill``) decompresses the cache per head instead; ``attend`` routes a
 step by its query count.
+
+A step with any number of query tokens per sequence, packed (a draft tree or chain
+to verify):
+
+    p = step_plan(cached_lens, new_lens, free_pages, free_head, block_table, T, parents, max_nodes)
+    rotary(q_r, p.positions, inv_freq, mscale, out=q_r)
+    append_kv_slots(ckv_new, kr_new, p.slots, ckv_pool, kr_pool, dims, p.positions, inv_freq, mscale)
+    out, lse = tree_attend(q_c, q_r, ckv_pool, kr_pool, block_table, p.seq_lens, p.cu_tokens,
+                           w_uk, w_uv, max_nodes, masks=p.masks)
 """
+import contextlib
 import ctypes
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -460,3 +471,294 @@ def attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, w_uk, w_uv, scale
     out, _, lse = decode(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, w_uk, w_uv,
                          scale=scale, stream=stream)
     return out, lse
+
+
+# ----------------------------------------------------------------------------
+# a step with any number of query tokens per sequence (include/mla_step.h)
+# ----------------------------------------------------------------------------
+
+TREE_MAX_NODES = 256
+STEP_MAX_BATCH = 16384
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+_ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _require(ok, what):
+    if not ok:
+        raise _b.MLAError(1, what)
+
+
+def _on(what, device, dtype, *tensors):
+    """Tensors (None allowed) of one device and type, contiguous."""
+    for t in tensors:
+        if t is not None:
+            _require(t.device == device and t.dtype == dtype and t.is_contiguous(),
+                     f"{what}: a contiguous {dtype} tensor on {device} is wanted")
+
+
+@contextlib.contextmanager
+def _switched(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:   # what a call allocates belongs to the stream that uses it
+            with torch.cuda.stream(stream):
+                yield
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _at(device, stream):
+    """The tensors' device made current for a call, with its stream if one is given."""
+    _require(device.type == "cuda", "the tensors are on a CUDA device")
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE
+    return _switched(device, stream)
+
+
+class StepPlan(NamedTuple):
+    """What step_plan lays out; see there."""
+    seq_lens: torch.Tensor
+    cu_tokens: torch.Tensor
+    seq_ids: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    free_head: torch.Tensor
+    masks: Optional[torch.Tensor]
+
+
+def alloc_step_plan(batch, num_tokens, device, max_nodes=0):
+    """An empty StepPlan, for step_plan(out=...) (a captured step keeps one); max_nodes > 0
+    includes the masks of a draft tree."""
+    i32 = dict(dtype=torch.int32, device=device)
+    words = (max_nodes + 31) // 32
+    return StepPlan(torch.empty(batch, **i32), torch.empty(batch + 1, **i32), torch.empty(num_tokens, **i32),
+                    torch.empty(num_tokens, **i32), torch.empty(num_tokens, dtype=torch.int64, device=device),
+                    torch.empty(1, **i32), torch.empty(num_tokens, words, **i32) if max_nodes > 0 else None)
+
+
+def step_plan(cached_lens, new_lens, free_pages, free_head, block_table, num_tokens, parents=None, max_nodes=0,
+              out=None, stream=None):
+    """The plan of a step, on the GPU: request b has cached_lens[b] tokens in the cache and adds
+    new_lens[b]. Fresh pages are taken from free_pages (from free_pages[free_head[0]] on) into
+    block_table, in place. Returns a StepPlan (all int32 but slots):
+
+      seq_lens [B]        cached + new
+      cu_tokens [B + 1]   first packed token of each request
+      seq_ids, positions, slots [num_tokens]   per packed token: request, rotary position, and cache
+                          slot (int64, page * 64 + row); -1 in rows behind the last request
+      free_head [1]       the first page still free
+      masks [num_tokens, ceil(max_nodes / 32)]   with parents: bits of the token and its ancestors
+
+    parents [num_tokens] int32: index within the request of the drafted token each token follows
+    (an earlier one; negative: it follows the context); max_nodes bounds new_lens then."""
+    B, max_pages = block_table.shape
+    dev = block_table.device
+    _on("step_plan", dev, torch.int32, cached_lens, new_lens, free_pages, free_head, block_table, parents)
+    _require(cached_lens.shape == (B,) and new_lens.shape == (B,) and free_head.numel() == 1 and
+             (parents is None or parents.numel() == num_tokens), "step_plan: sizes that do not fit")
+    _require(parents is None or 1 <= max_nodes <= TREE_MAX_NODES, "step_plan: max_nodes")
+    with _at(dev, stream):
+        if out is None:
+            out = alloc_step_plan(B, num_tokens, dev, max_nodes if parents is not None else 0)
+        else:
+            words = (max_nodes + 31) // 32
+            _on("step_plan", dev, torch.int32, *out[:4], out.free_head, out.masks)
+            _on("step_plan", dev, torch.int64, out.slots)
+            _require(out.seq_lens.shape == (B,) and out.cu_tokens.shape == (B + 1,) and out.free_head.numel() == 1 and
+                     all(t.shape == (num_tokens,) for t in out[2:5]) and
+                     (parents is None or (out.masks is not None and out.masks.shape == (num_tokens, words))),
+                     "step_plan: out of other sizes")
+        _b.check(_b.lib.mla_step_plan(_ptr(cached_lens), _ptr(new_lens), B, _ptr(free_pages), free_pages.numel(),
+                                      _ptr(free_head), _ptr(block_table), max_pages, _ptr(parents), max_nodes,
+                                      num_tokens, _ptr(out.seq_lens), _ptr(out.cu_tokens), _ptr(out.seq_ids),
+                                      _ptr(out.positions), _ptr(out.slots), _ptr(out.masks), _ptr(out.free_head),
+                                      _stream(stream)), "mla_step_plan")
+    return out
+
+
+def rope_frequencies(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_max=4096, beta_fast=32.0,
+                     beta_slow=1.0, device=None):
+    """(inv_freq [rot_dim / 2] float64 on `device`, mscale) of rotary positions scaled for long
+    contexts: "none", "linear" (position interpolation), "ntk" (a larger base) or "yarn" (by parts,
+    with its attention factor as mscale). Computed on the host; made once per model."""
+    _require(scaling in _ROPE_SCALINGS, f"rope_frequencies: scaling {scaling!r}")
+    _require(rot_dim > 0 and rot_dim % 2 == 0, "rope_frequencies: rot_dim")
+    freq = torch.empty(rot_dim // 2, dtype=torch.float64)
+    mscale = ctypes.c_double()
+    _b.check(_b.lib.mla_rope_frequencies(rot_dim, theta, _ROPE_SCALINGS[scaling], factor, original_max, beta_fast,
+                                         beta_slow, _ptr(freq), ctypes.addressof(mscale)), "mla_rope_frequencies")
+    return (freq if device is None else freq.to(device)), mscale.value
+
+
+def _rotary_tensor(x, out):
+    return _b.MLARotaryTensor(x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0), out.stride(1),
+                              x.shape[1])
+
+
+def rotary(x, positions, inv_freq, mscale=1.0, layout="interleaved", offset=0, inverse=False, out=None, k=None,
+           k_out=None, stream=None):
+    """x [T, heads, width] (bf16, fp16 or fp32; any token and head strides) with channels
+    offset .. offset + 2 len(inv_freq) of every head turned by positions[t] * inv_freq, pairs
+    (2i, 2i + 1) ("interleaved") or (i, i + half) ("half"), times mscale; the others are copied.
+    out=x turns in place; rows with a negative position are left as they are in `out` (zeros where it is
+    allocated here). inverse turns back: the gradient of x, given y's. k, a second tensor with heads of its
+    own (and k_out), goes with it in the same launch. Returns out, or (out, k_out)."""
+    both = [(x, out)] if k is None else [(x, out), (k, k_out)]
+    T, _, width = x.shape
+    dev = x.device
+    _require(layout in _ROPE_LAYOUTS and x.dtype in _DTYPES, f"rotary: layout {layout!r}, {x.dtype}")
+    _on("rotary", dev, torch.int32, positions)
+    _on("rotary", dev, torch.float64, inv_freq)
+    _require(positions.shape == (T,) and inv_freq.dim() == 1, "rotary: positions [T], inv_freq [rot / 2]")
+    with _at(dev, stream):
+        outs, args = [], []
+        for t, o in both:
+            if o is None:
+                o = torch.zeros(t.shape, dtype=t.dtype, device=t.device)
+            for v in (t, o):
+                _require(v.device == dev and v.dtype == x.dtype and v.dim() == 3 and v.shape[0] == T and
+                         v.shape[2] == width and (v.stride(2) == 1 or width == 1), "rotary: [T, heads, width] tensors")
+            _require(o.shape == t.shape, "rotary: out of another shape")
+            outs.append(o)
+            args.append(_rotary_tensor(t, o))
+        _b.check(_b.lib.mla_rotary(args[0], args[1] if k is not None else None, _DTYPES[x.dtype], T, width, offset,
+                                   2 * inv_freq.numel(), _ptr(positions), _ptr(inv_freq), mscale,
+                                   _ROPE_LAYOUTS[layout], int(inverse), _stream(stream)), "mla_rotary")
+    return outs[0] if k is None else tuple(outs)
+
+
+def _append_args(what, ckv_new, kr_new, slots, kr_pool, dims, positions, inv_freq, layout):
+    dev = ckv_new.device
+    T = ckv_new.shape[0]
+    _require(layout in _ROPE_LAYOUTS, f"{what}: layout {layout!r}")
+    for t, d in ((ckv_new, dims.d_latent), (kr_new, dims.d_rope)):
+        _require(t.device == dev and t.dtype == torch.bfloat16 and t.shape == (T, d) and t.stride(1) == 1,
+                 f"{what}: [T, {d}] bf16 rows")
+    _on(what, dev, torch.int64, slots)
+    _on(what, dev, torch.int32, positions)
+    _on(what, dev, torch.float64, inv_freq)
+    _require(slots.shape == (T,) and (positions is None or (positions.shape == (T,) and inv_freq is not None and
+                                                            inv_freq.numel() == dims.d_rope // 2)),
+             f"{what}: slots and positions [T], inv_freq [d_rope / 2]")
+    _require(kr_pool.device == dev and kr_pool.shape[1:] == (64, dims.d_rope), f"{what}: k_R pool")
+    return dev, T
+
+
+def append_kv_slots(ckv_new, kr_new, slots, ckv_pool, kr_pool, dims, positions=None, inv_freq=None, mscale=1.0,
+                    layout="interleaved", stream=None):
+    """Write new tokens into the paged pools (in place) by slot map: slots [T] int64 = page * 64 +
+    row, -1 for rows to skip (step_plan's). ckv_new [T, d_c] and kr_new [T, d_R] may be strided rows
+    (views of one projection). With positions [T] (and rope_frequencies' inv_freq, mscale) k_R is
+    turned on the way, else copied."""
+    dev, T = _append_args("append_kv_slots", ckv_new, kr_new, slots, kr_pool, dims, positions, inv_freq, layout)
+    _require(ckv_pool.device == dev and ckv_pool.shape == (kr_pool.shape[0], 64, dims.d_latent),
+             "append_kv_slots: c_KV pool")
+    with _at(dev, stream):
+        _b.check(_b.lib.mla_append_kv_slots(dims, _ptr(ckv_new), ckv_new.stride(0), _ptr(kr_new), kr_new.stride(0),
+                                            _ptr(slots), _ptr(positions), _ptr(inv_freq), mscale,
+                                            _ROPE_LAYOUTS[layout], T, _pool(ckv_pool), _pool(kr_pool),
+                                            ckv_pool.shape[0], _stream(stream)), "mla_append_kv_slots")
+
+
+def append_kv_slots_fp8(ckv_new, kr_new, slots, ckv8_pool, scales, kr_pool, dims, positions=None, inv_freq=None,
+                        mscale=1.0, layout="interleaved", stream=None):
+    """append_kv_slots quantising c_KV into the E4M3 cache (codes and per-token scales)."""
+    dev, T = _append_args("append_kv_slots_fp8", ckv_new, kr_new, slots, kr_pool, dims, positions, inv_freq, layout)
+    _require(ckv8_pool.device == dev and ckv8_pool.shape == (kr_pool.shape[0], 64, dims.d_latent),
+             "append_kv_slots_fp8: code pool")
+    _on("append_kv_slots_fp8", dev, torch.float32, scales)
+    _require(scales.shape == (kr_pool.shape[0], 64), "append_kv_slots_fp8: scales [pages, 64]")
+    with _at(dev, stream):
+        _b.check(_b.lib.mla_append_kv_slots_fp8(dims, _ptr(ckv_new), ckv_new.stride(0), _ptr(kr_new),
+                                                kr_new.stride(0), _ptr(slots), _ptr(positions), _ptr(inv_freq),
+                                                mscale, _ROPE_LAYOUTS[layout], T, _pool8(ckv8_pool), _ptr(scales),
+                                                _pool(kr_pool), ckv8_pool.shape[0], _stream(stream)),
+                 "mla_append_kv_slots_fp8")
+
+
+def tree_num_parts(dims, device=None):
+    """Partitions of a tree decode that fill the device."""
+    return _b.lib.mla_tree_num_parts(dims, _num_sms(torch.cuda.current_device() if device is None else device))
+
+
+def alloc_tree_workspace(dims, device, num_parts=None):
+    """Workspace of decode_tree for num_parts partitions (default: those that fill the device),
+    whatever the batch. Calls that may overlap on the GPU need one each."""
+    n = _b.lib.mla_tree_workspace_bytes(dims, tree_num_parts(dims, device) if num_parts is None else num_parts)
+    if n == 0:
+        raise _b.MLAError(2, "mla_tree_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _decode_tree(what, q, ckv_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks,
+                 num_parts, workspace, o_lat, lse_out, stream):
+    dev = q.device
+    T, H, D = q.shape
+    B, max_pages = block_table.shape
+    _on(what, dev, torch.bfloat16, q, o_lat)
+    _on(what, dev, torch.int32, block_table, seq_lens, cu_tokens, masks)
+    _on(what, dev, torch.float32, lse_out, scales)
+    _require(H == dims.num_heads and D == dims.d_latent + dims.d_rope, f"{what}: q [T, H, d_c + d_R]")
+    _require(seq_lens.shape == (B,) and cu_tokens.shape == (B + 1,), f"{what}: seq_lens [B], cu_tokens [B + 1]")
+    _require(masks is None or masks.shape == (T, (max_nodes + 31) // 32), f"{what}: masks [T, ceil(max_nodes / 32)]")
+    _require(kr_pool.device == dev and kr_pool.shape[1:] == (64, dims.d_rope), f"{what}: k_R pool")
+    _require(ckv_pool.device == dev and ckv_pool.shape == (kr_pool.shape[0], 64, dims.d_latent), f"{what}: c_KV pool")
+    with _at(dev, stream):
+        parts = tree_num_parts(dims, dev) if num_parts is None else num_parts
+        if workspace is None:
+            workspace = alloc_tree_workspace(dims, dev, parts)
+        _on(what, dev, torch.uint8, workspace)
+        if o_lat is None:
+            o_lat = torch.empty(T, H, dims.d_latent, dtype=torch.bfloat16, device=dev)
+        if lse_out is None:
+            lse_out = torch.empty(T, H, dtype=torch.float32, device=dev)
+        _require(o_lat.shape == (T, H, dims.d_latent) and lse_out.shape == (T, H), f"{what}: outputs of other sizes")
+        rest = (_pool(kr_pool), ckv_pool.shape[0], _ptr(block_table), max_pages, _ptr(seq_lens), _ptr(cu_tokens), B,
+                _ptr(masks), max_nodes, parts, _ptr(workspace), workspace.numel(), _ptr(o_lat), _ptr(lse_out),
+                _stream(stream))
+        if scales is None:
+            _b.check(_b.lib.mla_decode_tree(dims, _ptr(q), T, _pool(ckv_pool), *rest), "mla_decode_tree")
+        else:
+            _b.check(_b.lib.mla_decode_tree_fp8(dims, _ptr(q), T, _pool8(ckv_pool), _ptr(scales), *rest),
+                     "mla_decode_tree_fp8")
+    return o_lat, lse_out
+
+
+def decode_tree(q, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks=None, num_parts=None,
+                workspace=None, o_lat=None, lse_out=None, stream=None):
+    """Attention of packed query tokens q [T, H, d_c + d_R] (absorb_q's) over the paged latent cache:
+    sequence b's newest cu_tokens[b + 1] - cu_tokens[b] <= max_nodes tokens, each seeing the context and
+    the drafted tokens whose bit its mask sets (step_plan's masks; None: a chain). Returns
+    (o_lat [T, H, d_c] bf16, lse [T, H]); rows behind the last sequence are left as they were. Nothing is
+    read back from the device. workspace: alloc_tree_workspace's; one is allocated if None."""
+    return _decode_tree("decode_tree", q, ckv_pool, None, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes,
+                        masks, num_parts, workspace, o_lat, lse_out, stream)
+
+
+def decode_tree_fp8(q, ckv8_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks=None,
+                    num_parts=None, workspace=None, o_lat=None, lse_out=None, stream=None):
+    """decode_tree over the E4M3 cache (codes [pages, 64, 512] uint8, scales [pages, 64] fp32)."""
+    _require(scales.shape == ckv8_pool.shape[:2], "decode_tree_fp8: scales [pages, 64]")
+    return _decode_tree("decode_tree_fp8", q, ckv8_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims,
+                        max_nodes, masks, num_parts, workspace, o_lat, lse_out, stream)
+
+
+def tree_attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, w_uk, w_uv, max_nodes, masks=None,
+                scales=None, scale=0.0, workspace=None, stream=None):
+    """One attention step of packed query tokens q_c [T, H, d_n], q_r [T, H, d_R] (turned) over the
+    cache they are already in: absorb_q, decode_tree (over the E4M3 cache if its scales are given),
+    absorb_out. Returns (out [T, H, d_v], lse [T, H])."""
+    H, d_n, d_c = w_uk.shape
+    dims = make_dims(H, 1, d_n, d_c, q_r.shape[-1], w_uv.shape[-1], ckv_pool.shape[1], scale)
+    T, dev = q_c.shape[0], q_c.device
+    _on("tree_attend", dev, torch.bfloat16, q_c, q_r, w_uk, w_uv)
+    _require(q_c.shape == (T, H, d_n) and q_r.shape[:2] == (T, H) and w_uv.shape[:2] == (H, d_c),
+             "tree_attend: q_c [T, H, d_n], q_r [T, H, d_R], w_uk [H, d_n, d_c], w_uv [H, d_c, d_v]")
+    with _at(dev, stream):
+        q = absorb_q(q_c, q_r, w_uk, dims, stream=stream)
+        o_lat, lse = _decode_tree("tree_attend", q, ckv_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims,
+                                  max_nodes, masks, None, workspace, None, None, stream)
+        return absorb_out(o_lat, w_uv, dims, stream=stream), lse

@@ -3,7 +3,7 @@
     python -m mla_latent_kv_18_b200.build [--force] [--verbose]
 
 The library is a single translation unit (csrc/mla_api.cu includes every
-kernel) exporting the C ABI of include/mla_decode.h.
+kernel) exporting the C ABI of include/mla_decode.h and include/mla_step.h.
 """
 import os
 import subprocess
@@ -18,7 +18,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
 def _sources():
-    out = [os.path.join(INCLUDE, "mla_decode.h")]
+    out = [os.path.join(INCLUDE, f) for f in sorted(os.listdir(INCLUDE)) if f.endswith(".h")]
     for f in sorted(os.listdir(CSRC)):
         if f.endswith((".cu", ".cuh", ".h")):
             out.append(os.path.join(CSRC, f))

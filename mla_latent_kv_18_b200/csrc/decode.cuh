@@ -24,15 +24,22 @@
 //    CTA, cta_group::1, M = 128 rows; the 8-wide RoPE key is padded to the
 //    16-wide MMA K step with a zero core-matrix column in shared memory.
 //
+// Both are templates over the work they walk (kTree): whole sequences of n_q
+// query tokens with one partial result per (sequence, partition), or the row
+// blocks of a step with any number of query tokens per sequence under an ancestor
+// mask (tree_plan.cuh), where a block that one partition covers is final.
+//
 // Every wait is bounded (see wait_bounded); data errors set the device error
 // word. The kernels never read block-table entries past a sequence's last
 // page.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda.h>
 
 #include "common.cuh"
+#include "tree_plan.cuh"
 
 namespace mla {
 
@@ -53,7 +60,61 @@ struct DecodeArgs {
     int32_t rows;                // R = n_q * heads (<= 128)
     float scale;                 // softmax scale
     float scale_log2;            // scale * log2(e)
+    // kTree only: q, o_lat and lse_out are packed by token, the workspace holds
+    // 2 num_parts slots of item_rows rows
+    TreeBatch tree;
+    const uint32_t *masks;       // [total_tokens, mask_words] ancestor bits, or null (a chain)
+    __nv_bfloat16 *o_lat;        // [total_tokens, H, d_c]
+    float *lse_out;              // [total_tokens, H] or null
+    int32_t mask_words;
 };
+
+// Bit j: the query of drafted token `node` (of `nodes`) sees drafted token d + j.
+// Bits below a negative d (d > -32) are context tokens, which every node sees.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t *mask, int32_t words, int32_t node, int32_t nodes,
+                                              int32_t d) {
+    uint32_t bits;
+    if (!mask) {   // a chain: node i sees the drafted tokens 0 .. i
+        const int32_t n = node + 1 - d;
+        bits = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+    } else if (d < 0) {
+        bits = (mask[0] << -d) | ((1u << -d) - 1u);
+    } else {
+        const int32_t k = d >> 5;
+        const uint32_t lo = k < words ? mask[k] : 0u, hi = k + 1 < words ? mask[k + 1] : 0u;
+        bits = __funnelshift_r(lo, hi, d & 31);
+    }
+    const int32_t left = nodes - d;   // tokens before the sequence's end
+    return left >= 32 ? bits : left <= 0 ? 0u : bits & ((1u << left) - 1u);
+}
+
+// Of the 32 tokens from drafted index d on, those that are drafted tokens
+// (0 <= d + j < nodes) with a non-finite raw score in this lane's row. A latent
+// with a non-finite channel gives every row a non-finite score (0 * inf is NaN),
+// so each warp finds there the drafted latents that would poison, through the
+// value product's 0 * NaN, rows that do not see them.
+template <int N>
+__device__ __forceinline__ uint32_t odd_scores(const float (&s)[N], int off, int32_t d, int32_t nodes) {
+    uint32_t odd = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        odd |= ((__float_as_uint(s[off + j]) & 0x7F800000u) == 0x7F800000u ? 1u : 0u) << j;
+    const int32_t left = nodes - d;
+    if (left < 32) odd &= left <= 0 ? 0u : (1u << left) - 1u;
+    if (d < 0) odd &= d <= -32 ? 0u : ~0u << -d;
+    return odd;
+}
+
+// Eight bf16 with the non-finite ones set to zero.
+__device__ __forceinline__ uint4 finite_or_zero(uint4 v) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+        if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0x0000FFFFu;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 constexpr int kDecodeThreads = 192;          // single kernel: 6 warps
 constexpr int kPairThreads = 352;            // pair kernel: 11 warps (6 = P.V-slot producer, 7..10 segment warps)
@@ -191,6 +252,10 @@ constexpr uint32_t OFF_QSTAGE = OFF_PV + STAGE_PV;
 // and the segment warps first write there at that segment's end.
 constexpr int FIRST_PAGES = 4;
 constexpr uint32_t OFF_FIRST_PAGES = OFF_EPI;
+constexpr uint32_t OFF_FIRST_WALKER = OFF_EPI + 64;   // kTree: the walker at its first segment (every role
+                                                      // has copied it before a segment can end)
+constexpr int TREE_ROWS = 2 * ROWS_CTA;               // kTree: query rows per item
+constexpr int TREE_MIN_TILES = 8;                     // kTree: as the partition count of whole sequences
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TMEM_O = 0;                 // two 128-column accumulators (c = 0, 1)
 constexpr uint32_t TMEM_S = 256;               // three 32-column score buffers
@@ -238,8 +303,9 @@ struct Misc {
 static_assert(sizeof(Misc) <= pair::MISC_BYTES, "misc");
 
 // Tile-by-tile walk over a partition's segments.
+template <class Walker>
 struct TileCursor {
-    SegmentWalker w;
+    Walker w;
     bool have;
     int64_t t;   // tile index within sequence w.seg_b
     __device__ void start() {
@@ -334,8 +400,21 @@ __device__ __forceinline__ void dequant_slot(uint32_t slot, uint32_t blk, int wr
 // leader's barrier. The scales (32 consecutive tokens, from slot row sc_row0
 // on) arrive by TMA in the warp's own last row of block NBOX - 1, which the
 // warp itself overwrites in its first step, after reading them.
-template <int NBOX, int NPAIR>
-__device__ __forceinline__ bool dequant_tile(const TileCursor &cur, int64_t k, const DecodeArgs &args,
+// Where a segment's query rows are: rows q_row0 .. + seg_rows of plane q_seq of q
+// (kTree: q is one plane of packed rows).
+__device__ __forceinline__ int32_t q_row0(const SegmentWalker &) { return 0; }
+__device__ __forceinline__ int32_t q_row0(const TreeWalker &w) { return w.row0; }
+__device__ __forceinline__ int32_t q_seq(const SegmentWalker &w) { return w.seg_b; }
+__device__ __forceinline__ int32_t q_seq(const TreeWalker &) { return 0; }
+__device__ __forceinline__ int32_t seg_rows(const SegmentWalker &, const DecodeArgs &a) { return a.rows; }
+__device__ __forceinline__ int32_t seg_rows(const TreeWalker &w, const DecodeArgs &) { return w.rows; }
+__device__ __forceinline__ int64_t first_row(const SegmentWalker &w, const DecodeArgs &a) {
+    return static_cast<int64_t>(w.seg_b) * a.rows;
+}
+__device__ __forceinline__ int64_t first_row(const TreeWalker &w, const DecodeArgs &) { return w.row0; }
+
+template <int NBOX, int NPAIR, class Walker>
+__device__ __forceinline__ bool dequant_tile(const TileCursor<Walker> &cur, int64_t k, const DecodeArgs &args,
                                              uint32_t ring, uint32_t stage, uint32_t blk, int nst,
                                              uint64_t *codeb, uint64_t *fullb, int wrow0, int sc_row0,
                                              int tok_off, uint32_t rank, int lane,
@@ -365,7 +444,7 @@ __device__ __forceinline__ bool dequant_tile(const TileCursor &cur, int64_t k, c
     return true;
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kTree = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsFp8 : kPairThreads, 1)
     decode_pair_kernel(const __grid_constant__ CUtensorMap map_ckv32,
                        const __grid_constant__ CUtensorMap map_ckv64,
@@ -373,6 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                        const __grid_constant__ CUtensorMap map_sc,
                        const __grid_constant__ CUtensorMap map_q, const DecodeArgs args) {
     using namespace pair;
+    using Walker = std::conditional_t<kTree, TreeWalker, SegmentWalker>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = ptx::smem_u32(smem_raw);
     if (base & 1023u) {   // swizzled operands need a 1 KB aligned base; uniform over the cluster
@@ -434,7 +514,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
     // kernel of a decode step writes (the kernel ahead on the stream produces
     // q): it is made, down to this partition's first segment and that
     // segment's first page ids, before waiting for that kernel.
-    if (warp == 0) {
+    if (kTree && warp == 0) {
+        if constexpr (kTree) {
+            TreeWalker w0 = tree_start(args.tree, static_cast<int32_t>(part), args.num_parts, TOK, TREE_ROWS,
+                                       TREE_MIN_TILES);
+            w0.primed = w0.next();
+            if (lane == 0) {
+                *reinterpret_cast<TreeWalker *>(smem + OFF_FIRST_WALKER) = w0;
+                int32_t *pg = reinterpret_cast<int32_t *>(smem + OFF_FIRST_PAGES);
+                if (w0.primed) {   // the first page numbers, for the producers
+                    const int32_t *trow0 = args.block_table + static_cast<int64_t>(w0.seg_b) * args.max_pages;
+#pragma unroll
+                    for (int i = 0; i < FIRST_PAGES; ++i)
+                        pg[i] = (w0.t_begin + i < w0.t_end) ? trow0[w0.t_begin + i] : 0;
+                }
+                ptx::prefetch_tensormap(&map_ckv32);
+                ptx::prefetch_tensormap(&map_ckv64);
+                ptx::prefetch_tensormap(&map_kr32);
+                if (kFp8) ptx::prefetch_tensormap(&map_sc);
+                else ptx::prefetch_tensormap(&map_q);
+            }
+        }
+    } else if (warp == 0) {
         const SeqCursor c = find_sequence(args.seq_lens, args.batch, args.max_pages, args.n_q, TOK,
                                           P, -1);
         const int64_t N = c.total;   // plan cost
@@ -489,26 +590,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
     ptx::tc_fence_after();
     const uint32_t tmem = misc->tmem_base;
 
-    SegmentWalker walk;
-    walk.seq_lens = args.seq_lens;
-    walk.batch = args.batch;
-    walk.max_pages = args.max_pages;
-    walk.n_q = args.n_q;
-    walk.tile_tokens = TOK;
-    walk.N = misc->cur_N;
-    walk.P = misc->cur_P;
-    walk.p = part;
-    walk.b = misc->cur_b;
-    walk.O = misc->cur_O;
-    walk.S = misc->cur_S;
-    walk.te = (part < walk.P) ? part_start(part + 1, walk.N, walk.P) : 0;   // 0: idle partition
-    walk.tile = misc->first_tile;
-    walk.primed = misc->first_b >= 0;
-    walk.seg_b = misc->first_b;
-    walk.L = misc->first_L;
-    walk.t_begin = misc->first_t_begin;
-    walk.t_end = misc->first_t_end;
-    walk.slot = misc->first_slot;
+    Walker walk;
+    if constexpr (kTree) {
+        walk = *reinterpret_cast<const TreeWalker *>(smem + OFF_FIRST_WALKER);
+    } else {
+        walk.seq_lens = args.seq_lens;
+        walk.batch = args.batch;
+        walk.max_pages = args.max_pages;
+        walk.n_q = args.n_q;
+        walk.tile_tokens = TOK;
+        walk.N = misc->cur_N;
+        walk.P = misc->cur_P;
+        walk.p = part;
+        walk.b = misc->cur_b;
+        walk.O = misc->cur_O;
+        walk.S = misc->cur_S;
+        walk.te = (part < walk.P) ? part_start(part + 1, walk.N, walk.P) : 0;   // 0: idle partition
+        walk.tile = misc->first_tile;
+        walk.primed = misc->first_b >= 0;
+        walk.seg_b = misc->first_b;
+        walk.L = misc->first_L;
+        walk.t_begin = misc->first_t_begin;
+        walk.t_end = misc->first_t_end;
+        walk.slot = misc->first_slot;
+    }
 
     if (warp == 0 || warp == 6) {
         // ------------------------------------------------------ TMA producers
@@ -536,7 +641,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                 for (int j = 0; j < NB; ++j)
                     ptx::tma_load_3d(j < QT ? base + OFF_QSTAGE + j * (ROWS_CTA * 128)
                                             : base + OFF_Q + (j - QT) * (ROWS_CTA * 128),
-                                     &map_q, qbar, 64 * j, ROWS_CTA * static_cast<int>(rank), walk.seg_b);
+                                     &map_q, qbar, 64 * j, q_row0(walk) + ROWS_CTA * static_cast<int>(rank),
+                                     q_seq(walk));
             }
             bool first_seg = walk.primed;
             for (; !*abort_flag && walk.next(); first_seg = false) {
@@ -619,7 +725,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
         // three score buffers). Whichever is ready is issued; the polls are
         // non-blocking so a late KV tile never holds back a ready P.V.
         if (rank == 0 && ptx::elect_one()) {
-            SegmentWalker wq = walk, wp = walk;
+            Walker wq = walk, wp = walk;
             bool q_has = wq.next(), p_has = wp.next();
             int64_t tq = q_has ? wq.t_begin : 0, tp = p_has ? wp.t_begin : 0;
             int64_t kq = 0, kp = 0, gq = 0, gp = 0;
@@ -739,7 +845,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
             // 64, converting QK^T one tile ahead of P.V (the MMAs consume them in
             // that order); the scale copies hold the CTA's 32 QK^T tokens and
             // P.V tokens 32 (dq / 2) + [0, 32)
-            TileCursor cq, cp;
+            TileCursor<Walker> cq, cp;
             cq.w = walk;
             cq.start();
             cp = cq;
@@ -773,8 +879,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
         const int lt = q4 * 32 + lane;                 // TMEM lane 0..127
         const int row = lt & 63;                       // local query row
         const int half = lt >> 6;                      // which 128 channels of each MMA's 256
-        const int grow = ROWS_CTA * static_cast<int>(rank) + row;  // row within the sequence
-        const bool real_row = grow < args.rows;
+        const int grow = ROWS_CTA * static_cast<int>(rank) + row;  // row within the sequence (kTree: the item)
         const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
         const int st_tid = threadIdx.x - kSegWarp0 * 32;   // 0..127
         auto arrive_leader = [&](uint64_t *b) {
@@ -784,15 +889,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                 else ptx::mbar_arrive_cluster(leader_bar(b));
             }
         };
-        // Q of sequence b: channel blocks 0..5 into tensor memory in the
+        // Q of a segment: channel blocks 0..5 into tensor memory in the
         // duplicated 2-SM A layout (this lane holds row lt % 64, so lanes lt and
         // lt ^ 64 carry the same row), blocks 6..8 into shared memory
         // (128-byte swizzled, K-major).
         // The loads are issued in three rounds of independent requests (half of
         // the shared-memory blocks with each of the first two), so a segment
         // start costs three global-load latencies rather than one per block.
-        auto load_q = [&](int32_t b) {
-            const __nv_bfloat16 *qb = args.q + static_cast<int64_t>(b) * args.rows * D;
+        auto load_q = [&](const Walker &w) {
+            const __nv_bfloat16 *qb = args.q + first_row(w, args) * D;
+            const int32_t rows = seg_rows(w, args);
+            const bool real_row = grow < rows;
             const __nv_bfloat16 *qrow = qb + static_cast<int64_t>(real_row ? grow : 0) * D;
             constexpr int NSM = ROWS_CTA * (NB - QT) * 8 / 128 / 2;   // 8 + 8 chunks of blocks 5..8
 #pragma unroll 1
@@ -810,7 +917,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                         const int r = idx / ((NB - QT) * 8);
                         const int cc = idx - r * ((NB - QT) * 8);   // 16-byte chunk among blocks 5..8
                         const int gr = ROWS_CTA * static_cast<int>(rank) + r;
-                        sv[i] = (gr < args.rows)
+                        sv[i] = (gr < rows)
                                     ? ld_global_nc_v4(qb + static_cast<int64_t>(gr) * D + 64 * QT + cc * 8)
                                     : make_uint4(0, 0, 0, 0);
                     }
@@ -870,10 +977,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
             arrive_leader(&misc->q_ready);
         };
 
-        auto prefetch_q = [&](int32_t b) {   // the next segment's Q rows into L2
-            if (!real_row || half) return;
-            const char *qrow = reinterpret_cast<const char *>(
-                args.q + (static_cast<int64_t>(b) * args.rows + grow) * D);
+        auto prefetch_q = [&](const Walker &w) {   // the next segment's Q rows into L2
+            if (grow >= seg_rows(w, args) || half) return;
+            const char *qrow = reinterpret_cast<const char *>(args.q + (first_row(w, args) + grow) * D);
 #pragma unroll
             for (int i = 0; i < D * 2 / 128; ++i)
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(qrow + 128 * i));
@@ -883,20 +989,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
         int64_t g = 0;
         bool have = walk.next();
         if (have) {
-            if constexpr (kFp8) load_q(walk.seg_b);
+            if constexpr (kFp8) load_q(walk);
             else load_q_staged();
         }
         while (have && !*abort_flag) {
             const int64_t slot = walk.slot;
+            const int32_t rows = seg_rows(walk, args);
+            const bool real_row = grow < rows;
+            const int64_t out_row0 = kTree ? first_row(walk, args) : 0;
             const int64_t kl = k + (walk.t_end - walk.t_begin) - 1;   // the segment's last tile
             k = kl + 1;
             have = walk.next();
             if (have) {
-                prefetch_q(walk.seg_b);
+                prefetch_q(walk);
                 // the next segment's Q, once the last QK^T of this one is done
                 if (!wait_bounded<false>(bar(&misc->q_free), g & 1, abort_flag, args.timeout_ns)) break;
                 ptx::tc_fence_after();
-                load_q(walk.seg_b);
+                load_q(walk);
             }
             // this segment's partial result, once its last P.V is done
             if (!wait_bounded<false>(bar(&misc->seg_done), g & 1, abort_flag, args.timeout_ns)) break;
@@ -913,6 +1022,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
             // contiguous bytes instead of 32 rows x 16 bytes
             const uint32_t stg = base + OFF_EPI + static_cast<uint32_t>(warp - kSegWarp0) * 1024u;
             const int rr = lane >> 1, rc = lane & 1;   // read-back: rows rr + 16i, chunk rc
+            if (kTree && slot < 0) {
+                // the whole item: O / l is final, rounded to bf16 and stored (16 columns
+                // a piece through the same staging tile)
+#pragma unroll 1
+                for (int cch = 0; cch < 8; ++cch) {
+                    uint32_t o[32];
+                    ptx::tmem_ld32(tmem + lane_base + TMEM_O + 32 * cch, o);
+                    ptx::tmem_wait_ld();
+                    const int ch = 256 * (cch >> 2) + 128 * half + 32 * (cch & 3);
+#pragma unroll
+                    for (int pc = 0; pc < 2; ++pc) {
+                        uint32_t h[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            h[j] = pack_bf16x2(__uint_as_float(o[16 * pc + 2 * j]) * inv,
+                                               __uint_as_float(o[16 * pc + 2 * j + 1]) * inv);
+                        __syncwarp();   // the previous piece has been read back
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            st_shared_v4(stg + lane * 32 + ((c ^ ((lane >> 2) & 1)) << 4), h[4 * c], h[4 * c + 1],
+                                         h[4 * c + 2], h[4 * c + 3]);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int r = rr + 16 * i;
+                            const int grow_r = ROWS_CTA * static_cast<int>(rank) + ((q4 * 32 + r) & 63);
+                            const uint4 v = ld_shared_v4(stg + r * 32 + ((rc ^ ((r >> 2) & 1)) << 4));
+                            if (grow_r < rows)
+                                *reinterpret_cast<uint4 *>(args.o_lat + (out_row0 + grow_r) * DC + ch + 16 * pc +
+                                                           8 * rc) = v;
+                        }
+                    }
+                }
+            } else {
+            const int64_t slot_row0 = slot * (kTree ? TREE_ROWS : args.rows);
 #pragma unroll 1
             for (int cch = 0; cch < 8; ++cch) {
                 uint32_t o[32];
@@ -938,15 +1082,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                         const int r = rr + 16 * i;                        // staging row = lane r of this warp
                         const int grow_r = ROWS_CTA * static_cast<int>(rank) + ((q4 * 32 + r) & 63);
                         const uint4 v = ld_shared_v4(stg + r * 32 + ((rc ^ ((r >> 2) & 1)) << 4));
-                        if (grow_r < args.rows)
-                            *reinterpret_cast<uint4 *>(args.o_part + (slot * args.rows + grow_r) * DC + ch +
+                        if (grow_r < rows)
+                            *reinterpret_cast<uint4 *>(args.o_part + (slot_row0 + grow_r) * DC + ch +
                                                        8 * pc + 4 * rc) = v;
                     }
                 }
             }
+            }
             if (real_row && half == 0) {
-                args.lse_part[slot * args.rows + grow] =
-                    (l_row > 0.f) ? m_run * args.scale + logf(l_row) : -INFINITY;
+                // (kTree: a NaN sum stays NaN, so that the merge of a shared item keeps it)
+                const float lse = (kTree ? l_row != 0.f : l_row > 0.f) ? m_run * args.scale + logf(l_row) : -INFINITY;
+                if (!kTree || slot >= 0) args.lse_part[slot * (kTree ? TREE_ROWS : args.rows) + grow] = lse;
+                else if (args.lse_out) args.lse_out[out_row0 + grow] = lse;
             }
             ptx::tc_fence_before();
             arrive_leader(&misc->o_free);
@@ -958,9 +1105,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
         const int lt = q4 * 32 + lane;                 // TMEM lane 0..127
         const int row = lt & 63;                       // local query row
         const int half = lt >> 6;                      // which 32 tokens of the tile
-        const int grow = ROWS_CTA * static_cast<int>(rank) + row;  // row within the sequence
-        const bool real_row = grow < args.rows;
-        const int qi = real_row ? grow / args.heads : 0;
+        const int grow = ROWS_CTA * static_cast<int>(rank) + row;  // row within the sequence (kTree: the item)
         const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
         const int st_tid = threadIdx.x - kSoftmaxWarp0 * 32;   // 0..127
         auto arrive_leader = [&](uint64_t *b) {
@@ -979,13 +1124,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
             const int64_t slot = walk.slot;
             const int64_t k0 = k;
             const int64_t t_begin = walk.t_begin, t_end = walk.t_end;
-            const int32_t vis = real_row ? (L - args.n_q + qi + 1) : 0;
+            const bool real_row = grow < seg_rows(walk, args);
+            int32_t vis = 0;              // tokens of the sequence that this row sees (kTree: the context)
+            int32_t nodes = 0, node = 0;
+            const uint32_t *mask = nullptr;
+            if constexpr (kTree) {
+                nodes = walk.nodes;
+                vis = L - nodes;
+                const int32_t tok = real_row ? (walk.row0 + grow) / args.heads : walk.first_tok;
+                node = tok - walk.first_tok;
+                if (args.masks) mask = args.masks + static_cast<int64_t>(tok) * args.mask_words;
+            } else if (real_row) {
+                vis = L - args.n_q + grow / args.heads + 1;
+            }
             float m_run = -INFINITY;      // running max (raw score units)
             float l_run = 0.f;            // this lane's share of the row sum
             bool ok = true;
             for (int64_t t = t_begin; t < t_end; ++t, ++k) {
                 const int s = static_cast<int>(k & 1);          // P buffer, exchange words
                 const int sb = static_cast<int>(k % NSB);       // score buffer
+                const int32_t tok0 = static_cast<int32_t>(t) * TOK + half * OWN;
+                uint32_t bits = 0;   // kTree: which of the 32 tokens this row sees, read before the scores land
+                if (kTree && real_row)
+                    bits = tok0 + 32 <= vis ? ~0u : tree_bits(mask, args.mask_words, node, nodes, tok0 - vis);
                 if (!wait_bounded<false>(bar(&misc->s_full[sb]), (k / NSB) & 1, abort_flag,
                                          args.timeout_ns)) {
                     ok = false;
@@ -996,14 +1157,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                 ptx::tmem_ld32(tmem + lane_base + TMEM_S + 32 * sb, sr);
                 ptx::tmem_wait_ld();
 
-                const int32_t tok0 = static_cast<int32_t>(t) * TOK + half * OWN;
                 float v[32];
-                if (tok0 + 32 <= vis) {   // every token of this half visible: no mask
+                uint32_t odd = 0;   // kTree: drafted tokens with something non-finite in their latents
+                if (kTree && tok0 + 32 > vis) {   // the half holds drafted tokens (or the end)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(sr[j]);
+                    odd = __reduce_or_sync(0xffffffffu, odd_scores(v, 0, tok0 - vis, nodes));
+                }
+                if (kTree ? bits == ~0u : tok0 + 32 <= vis) {   // every token of this half visible: no mask
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(sr[j]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = (tok0 + j < vis) ? __uint_as_float(sr[j]) : -INFINITY;
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = (kTree ? (bits >> j) & 1u : tok0 + j < vis) ? __uint_as_float(sr[j]) : -INFINITY;
                 }
                 float mx = max_of<32>(v);
                 // Half-row maxima meet through tagged words: the lowest mantissa
@@ -1096,6 +1263,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                                      0u, 0u, 0u, 0u);
                     }
                 }
+                if (kTree && odd) {
+                    // The same for what is non-finite in a drafted token's latent, which some rows may
+                    // not see: cleared in this CTA's P.V slot (both warps of the half write the same).
+                    // (P.V of tile k - 2 is done: the wait cannot take that tile's landing for this one's.)
+                    const int ps = static_cast<int>(k % PV_STAGES);
+                    if (!wait_bounded(bar(&misc->pv_landed[ps]), (k / PV_STAGES) & 1, abort_flag,
+                                      args.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    for (; odd; odd &= odd - 1) {   // lane: 16 bytes of the token's 4 x 128
+                        const uint32_t at = base + OFF_PV + ps * STAGE_PV + (lane >> 3) * (TOK * 128) +
+                                            (half * OWN + __ffs(odd) - 1) * 128 + (lane & 7) * 16;
+                        const uint4 w = finite_or_zero(ld_shared_v4(at));
+                        st_shared_v4(at, w.x, w.y, w.z, w.w);
+                    }
+                }
                 ptx::fence_proxy_async_smem();
                 if (any_need) ptx::tc_fence_before();   // order the O rescale stores
                 arrive_leader(&misc->p_ready[s]);
@@ -1167,11 +1351,12 @@ static_assert(SMEM_BYTES <= 232448, "smem");
 static_assert((OFF_P % 1024) == 0 && (OFF_MISC % 1024) == 0, "align");
 }  // namespace single
 
-template <bool kSplit>
+template <bool kSplit, bool kTree = false>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
     decode_single_kernel(const __grid_constant__ CUtensorMap map_ckv,
                          const __grid_constant__ CUtensorMap map_kr, const DecodeArgs args) {
     using namespace single;
+    using Walker = std::conditional_t<kTree, TreeWalker, SegmentWalker>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw_base + 1023u) & ~1023u;
@@ -1183,6 +1368,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     const int lane = threadIdx.x & 31;
     const int64_t part = blockIdx.x;
     const int64_t P = args.num_parts;
+    constexpr int ITEM_ROWS = kSplit ? ROWS / 2 : ROWS;   // kTree: query rows per item
     auto bar = [&](const uint64_t *b) { return ptx::smem_u32(b); };
 
     if (threadIdx.x == 0) {
@@ -1215,7 +1401,20 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     // The plan reads only the sequence lengths, which no kernel of a decode step
     // writes: it is made, down to this partition's first segment, before
     // waiting for the kernel ahead on the stream (which produces q).
-    if (warp == 0) {
+    if (kTree && warp == 0) {
+        if constexpr (kTree) {
+            TreeWalker w0 = tree_start(args.tree, static_cast<int32_t>(part), args.num_parts, TOK, ITEM_ROWS, 1);
+            w0.primed = w0.next();
+            if (lane == 0) {
+                *reinterpret_cast<TreeWalker *>(misc->xtag) = w0;   // (the pair kernel's exchange words)
+                if (w0.primed)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                        args.block_table + static_cast<int64_t>(w0.seg_b) * args.max_pages + 2 * w0.t_begin));
+                ptx::prefetch_tensormap(&map_ckv);
+                ptx::prefetch_tensormap(&map_kr);
+            }
+        }
+    } else if (warp == 0) {
         const SeqCursor c = find_sequence(args.seq_lens, args.batch, args.max_pages, args.n_q, TOK,
                                           P, -1);
         const int64_t N = c.total;   // plan cost
@@ -1262,26 +1461,30 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = misc->tmem_base;
 
-    SegmentWalker walk;
-    walk.seq_lens = args.seq_lens;
-    walk.batch = args.batch;
-    walk.max_pages = args.max_pages;
-    walk.n_q = args.n_q;
-    walk.tile_tokens = TOK;
-    walk.N = misc->cur_N;
-    walk.P = misc->cur_P;
-    walk.p = part;
-    walk.b = misc->cur_b;
-    walk.O = misc->cur_O;
-    walk.S = misc->cur_S;
-    walk.te = (part < walk.P) ? part_start(part + 1, walk.N, walk.P) : 0;   // 0: idle partition
-    walk.tile = misc->first_tile;
-    walk.primed = misc->first_b >= 0;   // every role starts from the published first segment
-    walk.seg_b = misc->first_b;
-    walk.L = misc->first_L;
-    walk.t_begin = misc->first_t_begin;
-    walk.t_end = misc->first_t_end;
-    walk.slot = misc->first_slot;
+    Walker walk;
+    if constexpr (kTree) {
+        walk = *reinterpret_cast<const TreeWalker *>(misc->xtag);
+    } else {
+        walk.seq_lens = args.seq_lens;
+        walk.batch = args.batch;
+        walk.max_pages = args.max_pages;
+        walk.n_q = args.n_q;
+        walk.tile_tokens = TOK;
+        walk.N = misc->cur_N;
+        walk.P = misc->cur_P;
+        walk.p = part;
+        walk.b = misc->cur_b;
+        walk.O = misc->cur_O;
+        walk.S = misc->cur_S;
+        walk.te = (part < walk.P) ? part_start(part + 1, walk.N, walk.P) : 0;   // 0: idle partition
+        walk.tile = misc->first_tile;
+        walk.primed = misc->first_b >= 0;   // every role starts from the published first segment
+        walk.seg_b = misc->first_b;
+        walk.L = misc->first_L;
+        walk.t_begin = misc->first_t_begin;
+        walk.t_end = misc->first_t_end;
+        walk.slot = misc->first_slot;
+    }
 
     if (warp == 0) {
         if (ptx::elect_one()) {
@@ -1401,17 +1604,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         const int tl = q4 * 32 + lane;                  // TMEM lane = MMA row
         const int half = kSplit ? (lane >> 4) : 0;
         const int row = kSplit ? 16 * q4 + (lane & 15) : tl;   // query row
-        const bool real_row = row < args.rows;
-        const bool warp_real = (kSplit ? 16 * q4 : 32 * q4) < args.rows;   // warp holds a real row
-        const int qi = real_row ? row / args.heads : 0;
         const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
         const int st_tid = threadIdx.x - kSoftmaxWarp0 * 32;
         auto arrive = [&](uint64_t *b) {
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(b));
         };
-        auto load_q = [&](int32_t b) {   // all of a thread's loads in flight at once
-            const __nv_bfloat16 *qb = args.q + static_cast<int64_t>(b) * args.rows * D;
+        auto load_q = [&](const Walker &w) {   // all of a thread's loads in flight at once
+            const __nv_bfloat16 *qb = args.q + first_row(w, args) * D;
+            const int32_t rows = seg_rows(w, args);
             constexpr int QR = kSplit ? ROWS / 2 : ROWS;              // query rows held
             constexpr int NQ = (QR * (D / 8) + 127) / 128;           // chunks per thread
             uint4 v[NQ];
@@ -1420,8 +1621,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                 const int idx = st_tid + 128 * i;
                 const int r = idx / (D / 8);
                 const int cc = idx - r * (D / 8);
-                v[i] = (r < args.rows) ? ld_global_nc_v4(qb + static_cast<int64_t>(r) * D + cc * 8)
-                                       : make_uint4(0, 0, 0, 0);
+                v[i] = (r < rows) ? ld_global_nc_v4(qb + static_cast<int64_t>(r) * D + cc * 8)
+                                  : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
@@ -1444,13 +1645,28 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 
         int64_t k = 0;
         bool have = walk.next();
-        if (have) load_q(walk.seg_b);
+        if (have) load_q(walk);
         while (have && !*abort_flag) {
             const int32_t L = walk.L;
             const int64_t slot = walk.slot;
             const int64_t k0 = k;
             const int64_t t_begin = walk.t_begin, t_end = walk.t_end;
-            const int32_t vis = real_row ? (L - args.n_q + qi + 1) : 0;
+            const int32_t rows = seg_rows(walk, args);
+            const bool real_row = row < rows;
+            const bool warp_real = (kSplit ? 16 * q4 : 32 * q4) < rows;   // warp holds a real row
+            const int64_t out_row0 = kTree ? first_row(walk, args) : 0;
+            int32_t vis = 0;   // tokens of the sequence that this row sees (kTree: the context)
+            int32_t nodes = 0, node = 0;
+            const uint32_t *mask = nullptr;
+            if constexpr (kTree) {
+                nodes = walk.nodes;
+                vis = L - nodes;
+                const int32_t tok = real_row ? (walk.row0 + row) / args.heads : walk.first_tok;
+                node = tok - walk.first_tok;
+                if (args.masks) mask = args.masks + static_cast<int64_t>(tok) * args.mask_words;
+            } else if (real_row) {
+                vis = L - args.n_q + row / args.heads + 1;
+            }
             float m_run = -INFINITY, l_run = 0.f;
             bool ok = true;
             for (int64_t t = t_begin; t < t_end; ++t, ++k) {
@@ -1484,10 +1700,42 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                 ptx::tc_fence_before();
                 arrive(&misc->s_free[s]);
 
+                if (kTree && warp_real && (static_cast<int32_t>(t) + 1) * TOK > vis) {
+                    // drafted tokens in the tile: clear what is non-finite in their latents
+                    // (QK^T has read the stage, P.V waits for p_ready)
+                    const uint32_t st = base + OFF_STAGE + static_cast<int>(k % STAGES) * STAGE_BYTES;
+#pragma unroll
+                    for (int c = 0; c < TT / 32; ++c) {
+                        const int r0 = TT * half + 32 * c;
+                        uint32_t odd = odd_scores(v, 32 * c, static_cast<int32_t>(t) * TOK + r0 - vis, nodes);
+                        // (kSplit: lanes 0..15 hold the rows' tokens 0..63, lanes 16..31 the others)
+                        const uint32_t group = kSplit ? 0xFFFFu << (16 * half) : 0xFFFFFFFFu;
+                        odd = __reduce_or_sync(group, odd);
+                        for (; odd; odd &= odd - 1) {
+                            const uint32_t at = st + (r0 + __ffs(odd) - 1) * 128 + (lane & 7) * 16;
+                            const uint4 w = finite_or_zero(ld_shared_v4(at));
+                            st_shared_v4(at, w.x, w.y, w.z, w.w);
+                        }
+                    }
+                }
+
                 float alpha = 1.f;
                 if (warp_real) {
                     const int32_t tok0 = static_cast<int32_t>(t) * TOK + TT * half;
-                    if (tok0 + TT > vis) {   // mask the tokens this row does not see
+                    if constexpr (kTree) {
+                        if (!real_row || tok0 + TT > vis) {
+#pragma unroll
+                            for (int c = 0; c < TT / 32; ++c) {
+                                const int32_t d = tok0 + 32 * c - vis;
+                                const uint32_t bits = !real_row ? 0u
+                                                      : d <= -32 ? ~0u
+                                                                 : tree_bits(mask, args.mask_words, node, nodes, d);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    v[32 * c + j] = (bits >> j) & 1u ? v[32 * c + j] : -INFINITY;
+                            }
+                        }
+                    } else if (tok0 + TT > vis) {   // mask the tokens this row does not see
 #pragma unroll
                         for (int j = 0; j < TT; ++j) v[j] = (tok0 + j < vis) ? v[j] : -INFINITY;
                     }
@@ -1566,7 +1814,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             }
             if (!ok) break;
             have = walk.next();
-            if (have) load_q(walk.seg_b);
+            if (have) load_q(walk);
             const int64_t kl = k - 1;
             if (!wait_bounded(bar(&misc->pv_done[kl & 1]), (kl >> 1) & 1, abort_flag,
                               args.timeout_ns))
@@ -1577,7 +1825,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                 // same sum in both lanes); each lane writes one 32-channel half
                 const float l_row = kSplit ? l_run + __shfl_xor_sync(0xffffffffu, l_run, 16) : l_run;
                 const float inv = (l_row > 0.f) ? 1.f / l_row : 0.f;
-                float *dst = args.o_part + (slot * args.rows + row) * DC;
+                float *dst = args.o_part + (slot * (kTree ? ITEM_ROWS : args.rows) + row) * DC;
 #pragma unroll 1
                 for (int cch = 0; cch < DC / 32; ++cch) {
                     uint32_t o[32];
@@ -1591,7 +1839,20 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                             o[j] = __float_as_uint(half ? other + mine : mine + other);   // lane order: tokens 0..63 first
                         }
                     }
-                    if (real_row && (!kSplit || cch == half)) {
+                    if (kTree && slot < 0) {   // the whole item: O / l is final, rounded to bf16
+                        if (real_row && (!kSplit || cch == half)) {
+                            uint4 *d8 = reinterpret_cast<uint4 *>(args.o_lat + (out_row0 + row) * DC + 32 * cch);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t h[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    h[i] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * i]) * inv,
+                                                       __uint_as_float(o[8 * j + 2 * i + 1]) * inv);
+                                d8[j] = make_uint4(h[0], h[1], h[2], h[3]);
+                            }
+                        }
+                    } else if (real_row && (!kSplit || cch == half)) {
                         float4 *d4 = reinterpret_cast<float4 *>(dst + 32 * cch);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
@@ -1601,9 +1862,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                                                 __uint_as_float(o[4 * j + 3]) * inv);
                     }
                 }
-                if (real_row && half == 0)
-                    args.lse_part[slot * args.rows + row] =
-                        (l_row > 0.f) ? m_run * args.scale + logf(l_row) : -INFINITY;
+                if (real_row && half == 0) {
+                    // (kTree: a NaN sum stays NaN, so that the merge of a shared item keeps it)
+                    const float lse =
+                        (kTree ? l_row != 0.f : l_row > 0.f) ? m_run * args.scale + logf(l_row) : -INFINITY;
+                    if (!kTree || slot >= 0) args.lse_part[slot * (kTree ? ITEM_ROWS : args.rows) + row] = lse;
+                    else if (args.lse_out) args.lse_out[out_row0 + row] = lse;
+                }
             }
             ptx::tc_fence_before();
             arrive(&misc->o_free);

@@ -1150,3 +1150,5 @@ mla_status mla_gather_dequant_fp8(const mla_pool *ckv8, const float *scales, int
 }
 
 }  // extern "C"
+
+#include "step_api.cuh"

@@ -867,6 +867,42 @@ struct AppendArgs {
     int32_t T, d_c, d_r, batch, max_pages, num_pages, rotate;
 };
 
+// E4M3 with one fp32 scale per token: amax over the row, then
+// inv = 448 / amax, code = E4M3_rn_satfinite(x * inv), scale = amax / 448,
+// all with IEEE-rounded fp32 operations. The codes of one row of d_c bf16 go to
+// dst8; returns the scale. Warp-cooperative.
+__device__ __forceinline__ float quantise_row_e4m3(const uint4 *src, int32_t d_c, uint8_t *dst8, int lane) {
+    float amax = 0.f;
+    for (int i = lane; i < d_c / 8; i += 32) {
+        const uint4 v = src[i];
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 f = __bfloat1622float2(h[q]);
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 1.f;
+    for (int i = lane; i < d_c / 8; i += 32) {
+        const uint4 v = src[i];
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
+        uint32_t w[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float2 f0 = __bfloat1622float2(h[2 * q]), f1 = __bfloat1622float2(h[2 * q + 1]);
+            const uint32_t c0 = __nv_cvt_float_to_fp8(__fmul_rn(f0.x, inv), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t c1 = __nv_cvt_float_to_fp8(__fmul_rn(f0.y, inv), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t c2 = __nv_cvt_float_to_fp8(__fmul_rn(f1.x, inv), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t c3 = __nv_cvt_float_to_fp8(__fmul_rn(f1.y, inv), __NV_SATFINITE, __NV_E4M3);
+            w[q] = c0 | (c1 << 8) | (c2 << 16) | (c3 << 24);
+        }
+        *reinterpret_cast<uint2 *>(dst8 + 8 * i) = make_uint2(w[0], w[1]);
+    }
+    return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+}
+
 __global__ void __launch_bounds__(256) append_kv_kernel(const AppendArgs a) {
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -886,39 +922,9 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const AppendArgs a) {
     const int slot = pos % 64;
     const uint4 *src = reinterpret_cast<const uint4 *>(a.ckv_new + t * a.d_c);
     if (a.ckv8) {
-        // E4M3 with one fp32 scale per token: amax over the row, then
-        // inv = 448 / amax, code = E4M3_rn_satfinite(x * inv), scale = amax / 448,
-        // all with IEEE-rounded fp32 operations
-        float amax = 0.f;
-        for (int i = lane; i < a.d_c / 8; i += 32) {
-            const uint4 v = src[i];
-            const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 f = __bfloat1622float2(h[q]);
-                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 1.f;
-        uint8_t *dst8 = a.ckv8 + page * a.ckv_page_stride + slot * a.ckv_token_stride;
-        for (int i = lane; i < a.d_c / 8; i += 32) {
-            const uint4 v = src[i];
-            const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
-            uint32_t w[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float2 f0 = __bfloat1622float2(h[2 * q]), f1 = __bfloat1622float2(h[2 * q + 1]);
-                const uint32_t c0 = __nv_cvt_float_to_fp8(__fmul_rn(f0.x, inv), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t c1 = __nv_cvt_float_to_fp8(__fmul_rn(f0.y, inv), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t c2 = __nv_cvt_float_to_fp8(__fmul_rn(f1.x, inv), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t c3 = __nv_cvt_float_to_fp8(__fmul_rn(f1.y, inv), __NV_SATFINITE, __NV_E4M3);
-                w[q] = c0 | (c1 << 8) | (c2 << 16) | (c3 << 24);
-            }
-            *reinterpret_cast<uint2 *>(dst8 + 8 * i) = make_uint2(w[0], w[1]);
-        }
-        if (lane == 0) a.scales[static_cast<int64_t>(page) * 64 + slot] = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+        const float scale = quantise_row_e4m3(src, a.d_c, a.ckv8 + page * a.ckv_page_stride + slot * a.ckv_token_stride,
+                                              lane);
+        if (lane == 0) a.scales[static_cast<int64_t>(page) * 64 + slot] = scale;
     } else {
         uint4 *dst = reinterpret_cast<uint4 *>(a.ckv + page * a.ckv_page_stride + slot * a.ckv_token_stride);
         for (int i = lane; i < a.d_c / 8; i += 32) dst[i] = src[i];
