@@ -20,13 +20,13 @@ to verify):
     out, lse = tree_attend(q_c, q_r, ckv_pool, kr_pool, block_table, p.seq_lens, p.cu_tokens,
                            w_uk, w_uv, max_nodes, masks=p.masks)
 """
-import contextlib
 import ctypes
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _binding as _b
+from . import _step
 
 _NUM_SMS = {}
 
@@ -474,53 +474,15 @@ def attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, w_uk, w_uv, scale
 
 
 # ----------------------------------------------------------------------------
-# a step with any number of query tokens per sequence (include/mla_step.h)
-#
-# These calls are short on the GPU (a few microseconds for a step's tokens), so
-# their host side counts: the raw stream handle instead of a Stream object (0.1
-# against 3.1 us), plain integers for pointers, one allocation for a plan's outputs.
+# a step with any number of query tokens per sequence (include/mla_step.h). The
+# calls' checks, output allocation and launches are compiled (csrc/torch_step.cpp):
+# they run on their tensors' device and its current stream, or on `stream`.
 # ----------------------------------------------------------------------------
 
 TREE_MAX_NODES = 256
 STEP_MAX_BATCH = 16384
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
-_ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                      lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _require(ok, what):
-    if not ok:
-        raise _b.MLAError(1, what)
-
-
-def _on(what, index, dtype, *tensors):
-    """Tensors (None allowed) of one device and type, contiguous."""
-    for t in tensors:
-        if t is not None and (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()):
-            raise _b.MLAError(1, f"{what}: a contiguous {dtype} tensor on cuda:{index} is wanted")
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _elsewhere(index, stream):
-    """Whether a call has to change to its tensors' device, or to a given stream, first."""
-    _require(index >= 0, "the tensors are on a CUDA device")
-    return stream is not None or index != torch.cuda.current_device()
-
-
-@contextlib.contextmanager
-def _there(index, stream):
-    """The tensors' device, and the given stream: what a call allocates belongs to the stream it uses."""
-    with torch.cuda.device(index):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
+_step.types(_b.MLAError, _b.MLADims)
 
 
 class StepPlan(NamedTuple):
@@ -536,14 +498,12 @@ class StepPlan(NamedTuple):
 
 def alloc_step_plan(batch, num_tokens, device, max_nodes=0):
     """An empty StepPlan, for step_plan(out=...) (a captured step keeps one); max_nodes > 0
-    includes the masks of a draft tree. (The int32 tensors share one allocation.)"""
+    includes the masks of a draft tree."""
+    i32 = dict(dtype=torch.int32, device=device)
     words = (max_nodes + 31) // 32
-    sizes = [batch, batch + 1, num_tokens, num_tokens, 1]
-    if words:
-        sizes.append(num_tokens * words)
-    part = torch.empty(sum(sizes), dtype=torch.int32, device=device).split_with_sizes(sizes)
-    return StepPlan(part[0], part[1], part[2], part[3], torch.empty(num_tokens, dtype=torch.int64, device=device),
-                    part[4], part[5].view(num_tokens, words) if words else None)
+    return StepPlan(torch.empty(batch, **i32), torch.empty(batch + 1, **i32), torch.empty(num_tokens, **i32),
+                    torch.empty(num_tokens, **i32), torch.empty(num_tokens, dtype=torch.int64, device=device),
+                    torch.empty(1, **i32), torch.empty(num_tokens, words, **i32) if words else None)
 
 
 def step_plan(cached_lens, new_lens, free_pages, free_head, block_table, num_tokens, parents=None, max_nodes=0,
@@ -561,33 +521,12 @@ def step_plan(cached_lens, new_lens, free_pages, free_head, block_table, num_tok
 
     parents [num_tokens] int32: index within the request of the drafted token each token follows
     (an earlier one; negative: it follows the context); max_nodes bounds new_lens then."""
-    index = block_table.get_device()
-    if _elsewhere(index, stream):
-        with _there(index, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return step_plan(cached_lens, new_lens, free_pages, free_head, block_table, num_tokens, parents, max_nodes,
                              out)
-    B, max_pages = block_table.shape
-    _on("step_plan", index, torch.int32, cached_lens, new_lens, free_pages, free_head, block_table, parents)
-    tree = parents is not None
-    _require(cached_lens.shape == new_lens.shape == (B,) and free_head.numel() == 1 and
-             (not tree or (parents.numel() == num_tokens and 1 <= max_nodes <= TREE_MAX_NODES)),
-             "step_plan: cached_lens and new_lens [B], one free_head, parents [num_tokens], max_nodes in 1 .. 256")
-    if out is None:
-        out = alloc_step_plan(B, num_tokens, block_table.device, max_nodes if tree else 0)
-    else:
-        _on("step_plan", index, torch.int32, *out[:4], out.free_head, out.masks)
-        _on("step_plan", index, torch.int64, out.slots)
-        _require(out.seq_lens.shape == (B,) and out.cu_tokens.shape == (B + 1,) and out.free_head.numel() == 1 and
-                 all(t.shape == (num_tokens,) for t in out[2:5]) and
-                 (not tree or (out.masks is not None and out.masks.shape == (num_tokens, (max_nodes + 31) // 32))),
-                 "step_plan: out of other sizes")
-    _b.check(_b.lib.mla_step_plan(cached_lens.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(),
-                                  free_pages.numel(), free_head.data_ptr(), block_table.data_ptr(), max_pages,
-                                  _at(parents), max_nodes, num_tokens, out.seq_lens.data_ptr(),
-                                  out.cu_tokens.data_ptr(), out.seq_ids.data_ptr(), out.positions.data_ptr(),
-                                  out.slots.data_ptr(), _at(out.masks), out.free_head.data_ptr(), _raw_stream(index)),
-             "mla_step_plan")
-    return out
+    return StepPlan._make(_step.plan(cached_lens, new_lens, free_pages, free_head, block_table, num_tokens, parents,
+                                     max_nodes, out))
 
 
 def rope_frequencies(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_max=4096, beta_fast=32.0,
@@ -595,26 +534,14 @@ def rope_frequencies(rot_dim, theta=10000.0, scaling="none", factor=1.0, origina
     """(inv_freq [rot_dim / 2] float64 on `device`, mscale) of rotary positions scaled for long
     contexts: "none", "linear" (position interpolation), "ntk" (a larger base) or "yarn" (by parts,
     with its attention factor as mscale). Computed on the host; made once per model."""
-    _require(scaling in _ROPE_SCALINGS, f"rope_frequencies: scaling {scaling!r}")
-    _require(rot_dim > 0 and rot_dim % 2 == 0, "rope_frequencies: rot_dim")
+    if scaling not in _ROPE_SCALINGS or rot_dim <= 0 or rot_dim % 2:
+        raise _b.MLAError(1, f"rope_frequencies({rot_dim}, scaling={scaling!r})")
     freq = torch.empty(rot_dim // 2, dtype=torch.float64)
     mscale = ctypes.c_double()
     _b.check(_b.lib.mla_rope_frequencies(rot_dim, theta, _ROPE_SCALINGS[scaling], factor, original_max, beta_fast,
                                          beta_slow, freq.data_ptr(), ctypes.addressof(mscale)),
              "mla_rope_frequencies")
     return (freq if device is None else freq.to(device)), mscale.value
-
-
-def _rotary_tensor(x, out, like, index):
-    if out is None:
-        out = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
-    xs, os = x.stride(), out.stride()
-    shape = x.shape
-    _require(x.dtype is out.dtype is like.dtype and x.get_device() == out.get_device() == index and
-             len(shape) == 3 and shape == out.shape and shape[0] == like.shape[0] and shape[2] == like.shape[2] and
-             (xs[2] == os[2] == 1 or shape[2] == 1),
-             "rotary: [T, heads, width] tensors of one type, tokens and width, out of the same shape")
-    return out, _b.MLARotaryTensor(x.data_ptr(), out.data_ptr(), xs[0], xs[1], os[0], os[1], shape[1])
 
 
 def rotary(x, positions, inv_freq, mscale=1.0, layout="interleaved", offset=0, inverse=False, out=None, k=None,
@@ -625,58 +552,10 @@ def rotary(x, positions, inv_freq, mscale=1.0, layout="interleaved", offset=0, i
     out=x turns in place; rows with a negative position are left as they are in `out` (zeros where it is
     allocated here). inverse turns back: the gradient of x, given y's. k, a second tensor with heads of its
     own (and k_out), goes with it in the same launch. Returns out, or (out, k_out)."""
-    index = x.get_device()
-    if _elsewhere(index, stream):
-        with _there(index, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return rotary(x, positions, inv_freq, mscale, layout, offset, inverse, out, k, k_out)
-    dtype, order = _DTYPES.get(x.dtype), _ROPE_LAYOUTS.get(layout)
-    _require(dtype is not None and order is not None, f"rotary: layout {layout!r}, {x.dtype}")
-    _on("rotary", index, torch.int32, positions)
-    _on("rotary", index, torch.float64, inv_freq)
-    out, first = _rotary_tensor(x, out, x, index)
-    T, _, width = x.shape
-    _require(positions.shape == (T,) and inv_freq.dim() == 1, "rotary: positions [T], inv_freq [rot / 2]")
-    second = None
-    if k is not None:
-        k_out, second = _rotary_tensor(k, k_out, x, index)
-    _b.check(_b.lib.mla_rotary(first, second, dtype, T, width, offset, 2 * inv_freq.numel(), positions.data_ptr(),
-                               inv_freq.data_ptr(), mscale, order, int(inverse), _raw_stream(index)), "mla_rotary")
-    return out if k is None else (out, k_out)
-
-
-def _pools(what, index, dims, ckv_pool, dtype, kr_pool):
-    """A c_KV (or code) pool and a k_R pool of the same pages as mla_pool structs."""
-    c, k, cs, ks = ckv_pool.shape, kr_pool.shape, ckv_pool.stride(), kr_pool.stride()
-    _require(ckv_pool.dtype is dtype and kr_pool.dtype is torch.bfloat16 and
-             ckv_pool.get_device() == kr_pool.get_device() == index and len(c) == len(k) == 3 and c[0] == k[0] and
-             c[1] == k[1] == 64 and c[2] == dims.d_latent and k[2] == dims.d_rope and cs[2] == ks[2] == 1,
-             f"{what}: pools [pages, 64, d_c] and [pages, 64, d_R] on one device")
-    return (_b.MLAPool(ckv_pool.data_ptr(), cs[0], cs[1]), _b.MLAPool(kr_pool.data_ptr(), ks[0], ks[1]), c[0])
-
-
-def _append_slots(what, ckv_new, kr_new, slots, ckv_pool, scales, kr_pool, dims, positions, inv_freq, mscale, layout):
-    index = ckv_new.get_device()
-    order = _ROPE_LAYOUTS.get(layout)
-    _require(order is not None, f"{what}: layout {layout!r}")
-    c, k, T = ckv_new.stride(), kr_new.stride(), slots.numel()
-    _require(ckv_new.dtype is kr_new.dtype is torch.bfloat16 and kr_new.get_device() == index and
-             ckv_new.shape == (T, dims.d_latent) and kr_new.shape == (T, dims.d_rope) and c[1] == k[1] == 1,
-             f"{what}: ckv_new [T, d_c] and kr_new [T, d_R] bf16 rows, slots [T]")
-    _on(what, index, torch.int64, slots)
-    _on(what, index, torch.int32, positions)
-    _on(what, index, torch.float64, inv_freq)
-    _require(positions is None or (positions.numel() == T and inv_freq is not None and
-                                   2 * inv_freq.numel() == dims.d_rope), f"{what}: positions [T], inv_freq [d_R / 2]")
-    cp, kp, pages = _pools(what, index, dims, ckv_pool, torch.bfloat16 if scales is None else torch.uint8, kr_pool)
-    head = (dims, ckv_new.data_ptr(), c[0], kr_new.data_ptr(), k[0], slots.data_ptr(), _at(positions), _at(inv_freq),
-            mscale, order, T, cp)
-    if scales is None:
-        _b.check(_b.lib.mla_append_kv_slots(*head, kp, pages, _raw_stream(index)), "mla_append_kv_slots")
-    else:
-        _on(what, index, torch.float32, scales)
-        _require(scales.shape == (pages, 64), f"{what}: scales [pages, 64]")
-        _b.check(_b.lib.mla_append_kv_slots_fp8(*head, scales.data_ptr(), kp, pages, _raw_stream(index)),
-                 "mla_append_kv_slots_fp8")
+    return _step.rotary(x, positions, inv_freq, mscale, layout, offset, inverse, out, k, k_out)
 
 
 def append_kv_slots(ckv_new, kr_new, slots, ckv_pool, kr_pool, dims, positions=None, inv_freq=None, mscale=1.0,
@@ -685,24 +564,22 @@ def append_kv_slots(ckv_new, kr_new, slots, ckv_pool, kr_pool, dims, positions=N
     row, -1 for rows to skip (step_plan's). ckv_new [T, d_c] and kr_new [T, d_R] may be strided rows
     (views of one projection). With positions [T] (and rope_frequencies' inv_freq, mscale) k_R is
     turned on the way, else copied."""
-    index = ckv_new.get_device()
-    if _elsewhere(index, stream):
-        with _there(index, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return append_kv_slots(ckv_new, kr_new, slots, ckv_pool, kr_pool, dims, positions, inv_freq, mscale, layout)
-    _append_slots("append_kv_slots", ckv_new, kr_new, slots, ckv_pool, None, kr_pool, dims, positions, inv_freq, mscale,
-                  layout)
+    _step.append(ckv_new, kr_new, slots, ckv_pool, None, kr_pool, dims, positions, inv_freq, mscale, layout)
 
 
 def append_kv_slots_fp8(ckv_new, kr_new, slots, ckv8_pool, scales, kr_pool, dims, positions=None, inv_freq=None,
                         mscale=1.0, layout="interleaved", stream=None):
     """append_kv_slots quantising c_KV into the E4M3 cache (codes and per-token scales)."""
-    index = ckv_new.get_device()
-    if _elsewhere(index, stream):
-        with _there(index, stream):
+    if scales is None:
+        raise _b.MLAError(1, "append_kv_slots_fp8: scales [pages, 64]")
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return append_kv_slots_fp8(ckv_new, kr_new, slots, ckv8_pool, scales, kr_pool, dims, positions, inv_freq,
                                        mscale, layout)
-    _append_slots("append_kv_slots_fp8", ckv_new, kr_new, slots, ckv8_pool, scales, kr_pool, dims, positions, inv_freq,
-                  mscale, layout)
+    _step.append(ckv_new, kr_new, slots, ckv8_pool, scales, kr_pool, dims, positions, inv_freq, mscale, layout)
 
 
 def tree_num_parts(dims, device=None):
@@ -719,41 +596,6 @@ def alloc_tree_workspace(dims, device, num_parts=None):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _decode_tree(what, q, ckv_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks,
-                 num_parts, workspace, o_lat, lse_out):
-    index, device = q.get_device(), q.device
-    T, H, D = q.shape
-    B, max_pages = block_table.shape
-    d_c = dims.d_latent
-    _on(what, index, torch.bfloat16, q, o_lat)
-    _on(what, index, torch.int32, block_table, seq_lens, cu_tokens, masks)
-    _on(what, index, torch.float32, lse_out, scales)
-    _on(what, index, torch.uint8, workspace)
-    _require(H == dims.num_heads and D == d_c + dims.d_rope and seq_lens.shape == (B,) and
-             cu_tokens.shape == (B + 1,) and (masks is None or masks.shape == (T, (max_nodes + 31) // 32)),
-             f"{what}: q [T, H, d_c + d_R], seq_lens [B], cu_tokens [B + 1], masks [T, ceil(max_nodes / 32)]")
-    cp, kp, pages = _pools(what, index, dims, ckv_pool, torch.bfloat16 if scales is None else torch.uint8, kr_pool)
-    if num_parts is None:
-        num_parts = _b.lib.mla_tree_num_parts(dims, _NUM_SMS.get(index) or _num_sms(device))
-    if workspace is None:
-        workspace = alloc_tree_workspace(dims, device, num_parts)
-    if o_lat is None:
-        o_lat = torch.empty(T, H, d_c, dtype=torch.bfloat16, device=device)
-    if lse_out is None:
-        lse_out = torch.empty(T, H, dtype=torch.float32, device=device)
-    _require(o_lat.shape == (T, H, d_c) and lse_out.shape == (T, H), f"{what}: o_lat [T, H, d_c], lse_out [T, H]")
-    rest = (kp, pages, block_table.data_ptr(), max_pages, seq_lens.data_ptr(), cu_tokens.data_ptr(), B, _at(masks),
-            max_nodes, num_parts, workspace.data_ptr(), workspace.numel(), o_lat.data_ptr(), lse_out.data_ptr(),
-            _raw_stream(index))
-    if scales is None:
-        _b.check(_b.lib.mla_decode_tree(dims, q.data_ptr(), T, cp, *rest), "mla_decode_tree")
-    else:
-        _require(scales.shape == (pages, 64), f"{what}: scales [pages, 64]")
-        _b.check(_b.lib.mla_decode_tree_fp8(dims, q.data_ptr(), T, cp, scales.data_ptr(), *rest),
-                 "mla_decode_tree_fp8")
-    return o_lat, lse_out
-
-
 def decode_tree(q, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks=None, num_parts=None,
                 workspace=None, o_lat=None, lse_out=None, stream=None):
     """Attention of packed query tokens q [T, H, d_c + d_R] (absorb_q's) over the paged latent cache:
@@ -761,26 +603,25 @@ def decode_tree(q, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, dims, ma
     the drafted tokens whose bit its mask sets (step_plan's masks; None: a chain). Returns
     (o_lat [T, H, d_c] bf16, lse [T, H]); rows behind the last sequence are left as they were. Nothing is
     read back from the device. workspace: alloc_tree_workspace's; one is allocated if None."""
-    index = q.get_device()
-    if _elsewhere(index, stream):
-        with _there(index, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return decode_tree(q, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks, num_parts,
                                workspace, o_lat, lse_out)
-    return _decode_tree("decode_tree", q, ckv_pool, None, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes,
-                        masks, num_parts, workspace, o_lat, lse_out)
+    return _step.tree(q, ckv_pool, None, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks, num_parts,
+                      workspace, o_lat, lse_out)
 
 
 def decode_tree_fp8(q, ckv8_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks=None,
                     num_parts=None, workspace=None, o_lat=None, lse_out=None, stream=None):
     """decode_tree over the E4M3 cache (codes [pages, 64, 512] uint8, scales [pages, 64] fp32)."""
-    index = q.get_device()
-    if _elsewhere(index, stream):
-        with _there(index, stream):
+    if scales is None:
+        raise _b.MLAError(1, "decode_tree_fp8: scales [pages, 64]")
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return decode_tree_fp8(q, ckv8_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes,
                                    masks, num_parts, workspace, o_lat, lse_out)
-    _require(scales is not None, "decode_tree_fp8: scales [pages, 64]")
-    return _decode_tree("decode_tree_fp8", q, ckv8_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims,
-                        max_nodes, masks, num_parts, workspace, o_lat, lse_out)
+    return _step.tree(q, ckv8_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks, num_parts,
+                      workspace, o_lat, lse_out)
 
 
 def tree_attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, w_uk, w_uv, max_nodes, masks=None,
@@ -788,18 +629,18 @@ def tree_attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, w
     """One attention step of packed query tokens q_c [T, H, d_n], q_r [T, H, d_R] (turned) over the
     cache they are already in: absorb_q, decode_tree (over the E4M3 cache if its scales are given),
     absorb_out. Returns (out [T, H, d_v], lse [T, H])."""
-    index = q_c.get_device()
-    if _elsewhere(index, stream):
-        with _there(index, stream):
+    if stream is not None or q_c.device.index != torch.cuda.current_device():
+        with torch.cuda.device(q_c.device), torch.cuda.stream(stream):
             return tree_attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, w_uk, w_uv, max_nodes,
                                masks, scales, scale, workspace)
     H, d_n, d_c = w_uk.shape
-    dims = make_dims(H, 1, d_n, d_c, q_r.shape[-1], w_uv.shape[-1], ckv_pool.shape[1], scale)
-    T = q_c.shape[0]
-    _on("tree_attend", index, torch.bfloat16, q_c, q_r, w_uk, w_uv)
-    _require(q_c.shape == (T, H, d_n) and q_r.shape[:2] == (T, H) and w_uv.shape[:2] == (H, d_c),
-             "tree_attend: q_c [T, H, d_n], q_r [T, H, d_R], w_uk [H, d_n, d_c], w_uv [H, d_c, d_v]")
+    T, d_r, d_v = q_c.shape[0], q_r.shape[-1], w_uv.shape[-1]
+    for t, shape in ((q_c, (T, H, d_n)), (q_r, (T, H, d_r)), (w_uk, (H, d_n, d_c)), (w_uv, (H, d_c, d_v))):
+        if t.dtype != torch.bfloat16 or t.device != q_c.device or t.shape != shape or not t.is_contiguous():
+            raise _b.MLAError(1, "tree_attend: contiguous bf16 q_c [T, H, d_n], q_r [T, H, d_R], w_uk [H, d_n, d_c], "
+                                 "w_uv [H, d_c, d_v] on one device")
+    dims = make_dims(H, 1, d_n, d_c, d_r, d_v, ckv_pool.shape[1], scale)
     q = absorb_q(q_c, q_r, w_uk, dims)
-    o_lat, lse = _decode_tree("tree_attend", q, ckv_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims,
-                              max_nodes, masks, None, workspace, None, None)
+    o_lat, lse = _step.tree(q, ckv_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks, None,
+                            workspace, None, None)
     return absorb_out(o_lat, w_uv, dims), lse
