@@ -1351,12 +1351,11 @@ static_assert(SMEM_BYTES <= 232448, "smem");
 static_assert((OFF_P % 1024) == 0 && (OFF_MISC % 1024) == 0, "align");
 }  // namespace single
 
-template <bool kSplit, bool kTree = false>
+template <bool kSplit>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
     decode_single_kernel(const __grid_constant__ CUtensorMap map_ckv,
                          const __grid_constant__ CUtensorMap map_kr, const DecodeArgs args) {
     using namespace single;
-    using Walker = std::conditional_t<kTree, TreeWalker, SegmentWalker>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw_base + 1023u) & ~1023u;
@@ -1368,7 +1367,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     const int lane = threadIdx.x & 31;
     const int64_t part = blockIdx.x;
     const int64_t P = args.num_parts;
-    constexpr int ITEM_ROWS = kSplit ? ROWS / 2 : ROWS;   // kTree: query rows per item
     auto bar = [&](const uint64_t *b) { return ptx::smem_u32(b); };
 
     if (threadIdx.x == 0) {
@@ -1401,20 +1399,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     // The plan reads only the sequence lengths, which no kernel of a decode step
     // writes: it is made, down to this partition's first segment, before
     // waiting for the kernel ahead on the stream (which produces q).
-    if (kTree && warp == 0) {
-        if constexpr (kTree) {
-            TreeWalker w0 = tree_start(args.tree, static_cast<int32_t>(part), args.num_parts, TOK, ITEM_ROWS, 1);
-            w0.primed = w0.next();
-            if (lane == 0) {
-                *reinterpret_cast<TreeWalker *>(misc->xtag) = w0;   // (the pair kernel's exchange words)
-                if (w0.primed)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
-                        args.block_table + static_cast<int64_t>(w0.seg_b) * args.max_pages + 2 * w0.t_begin));
-                ptx::prefetch_tensormap(&map_ckv);
-                ptx::prefetch_tensormap(&map_kr);
-            }
-        }
-    } else if (warp == 0) {
+    if (warp == 0) {
         const SeqCursor c = find_sequence(args.seq_lens, args.batch, args.max_pages, args.n_q, TOK,
                                           P, -1);
         const int64_t N = c.total;   // plan cost
@@ -1461,30 +1446,26 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = misc->tmem_base;
 
-    Walker walk;
-    if constexpr (kTree) {
-        walk = *reinterpret_cast<const TreeWalker *>(misc->xtag);
-    } else {
-        walk.seq_lens = args.seq_lens;
-        walk.batch = args.batch;
-        walk.max_pages = args.max_pages;
-        walk.n_q = args.n_q;
-        walk.tile_tokens = TOK;
-        walk.N = misc->cur_N;
-        walk.P = misc->cur_P;
-        walk.p = part;
-        walk.b = misc->cur_b;
-        walk.O = misc->cur_O;
-        walk.S = misc->cur_S;
-        walk.te = (part < walk.P) ? part_start(part + 1, walk.N, walk.P) : 0;   // 0: idle partition
-        walk.tile = misc->first_tile;
-        walk.primed = misc->first_b >= 0;   // every role starts from the published first segment
-        walk.seg_b = misc->first_b;
-        walk.L = misc->first_L;
-        walk.t_begin = misc->first_t_begin;
-        walk.t_end = misc->first_t_end;
-        walk.slot = misc->first_slot;
-    }
+    SegmentWalker walk;
+    walk.seq_lens = args.seq_lens;
+    walk.batch = args.batch;
+    walk.max_pages = args.max_pages;
+    walk.n_q = args.n_q;
+    walk.tile_tokens = TOK;
+    walk.N = misc->cur_N;
+    walk.P = misc->cur_P;
+    walk.p = part;
+    walk.b = misc->cur_b;
+    walk.O = misc->cur_O;
+    walk.S = misc->cur_S;
+    walk.te = (part < walk.P) ? part_start(part + 1, walk.N, walk.P) : 0;   // 0: idle partition
+    walk.tile = misc->first_tile;
+    walk.primed = misc->first_b >= 0;   // every role starts from the published first segment
+    walk.seg_b = misc->first_b;
+    walk.L = misc->first_L;
+    walk.t_begin = misc->first_t_begin;
+    walk.t_end = misc->first_t_end;
+    walk.slot = misc->first_slot;
 
     if (warp == 0) {
         if (ptx::elect_one()) {
@@ -1604,15 +1585,17 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         const int tl = q4 * 32 + lane;                  // TMEM lane = MMA row
         const int half = kSplit ? (lane >> 4) : 0;
         const int row = kSplit ? 16 * q4 + (lane & 15) : tl;   // query row
+        const bool real_row = row < args.rows;
+        const bool warp_real = (kSplit ? 16 * q4 : 32 * q4) < args.rows;   // warp holds a real row
+        const int qi = real_row ? row / args.heads : 0;
         const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
         const int st_tid = threadIdx.x - kSoftmaxWarp0 * 32;
         auto arrive = [&](uint64_t *b) {
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(b));
         };
-        auto load_q = [&](const Walker &w) {   // all of a thread's loads in flight at once
-            const __nv_bfloat16 *qb = args.q + first_row(w, args) * D;
-            const int32_t rows = seg_rows(w, args);
+        auto load_q = [&](int32_t b) {   // all of a thread's loads in flight at once
+            const __nv_bfloat16 *qb = args.q + static_cast<int64_t>(b) * args.rows * D;
             constexpr int QR = kSplit ? ROWS / 2 : ROWS;              // query rows held
             constexpr int NQ = (QR * (D / 8) + 127) / 128;           // chunks per thread
             uint4 v[NQ];
@@ -1621,8 +1604,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                 const int idx = st_tid + 128 * i;
                 const int r = idx / (D / 8);
                 const int cc = idx - r * (D / 8);
-                v[i] = (r < rows) ? ld_global_nc_v4(qb + static_cast<int64_t>(r) * D + cc * 8)
-                                  : make_uint4(0, 0, 0, 0);
+                v[i] = (r < args.rows) ? ld_global_nc_v4(qb + static_cast<int64_t>(r) * D + cc * 8)
+                                       : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
@@ -1645,28 +1628,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 
         int64_t k = 0;
         bool have = walk.next();
-        if (have) load_q(walk);
+        if (have) load_q(walk.seg_b);
         while (have && !*abort_flag) {
             const int32_t L = walk.L;
             const int64_t slot = walk.slot;
             const int64_t k0 = k;
             const int64_t t_begin = walk.t_begin, t_end = walk.t_end;
-            const int32_t rows = seg_rows(walk, args);
-            const bool real_row = row < rows;
-            const bool warp_real = (kSplit ? 16 * q4 : 32 * q4) < rows;   // warp holds a real row
-            const int64_t out_row0 = kTree ? first_row(walk, args) : 0;
-            int32_t vis = 0;   // tokens of the sequence that this row sees (kTree: the context)
-            int32_t nodes = 0, node = 0;
-            const uint32_t *mask = nullptr;
-            if constexpr (kTree) {
-                nodes = walk.nodes;
-                vis = L - nodes;
-                const int32_t tok = real_row ? (walk.row0 + row) / args.heads : walk.first_tok;
-                node = tok - walk.first_tok;
-                if (args.masks) mask = args.masks + static_cast<int64_t>(tok) * args.mask_words;
-            } else if (real_row) {
-                vis = L - args.n_q + row / args.heads + 1;
-            }
+            const int32_t vis = real_row ? (L - args.n_q + qi + 1) : 0;
             float m_run = -INFINITY, l_run = 0.f;
             bool ok = true;
             for (int64_t t = t_begin; t < t_end; ++t, ++k) {
@@ -1700,42 +1668,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                 ptx::tc_fence_before();
                 arrive(&misc->s_free[s]);
 
-                if (kTree && warp_real && (static_cast<int32_t>(t) + 1) * TOK > vis) {
-                    // drafted tokens in the tile: clear what is non-finite in their latents
-                    // (QK^T has read the stage, P.V waits for p_ready)
-                    const uint32_t st = base + OFF_STAGE + static_cast<int>(k % STAGES) * STAGE_BYTES;
-#pragma unroll
-                    for (int c = 0; c < TT / 32; ++c) {
-                        const int r0 = TT * half + 32 * c;
-                        uint32_t odd = odd_scores(v, 32 * c, static_cast<int32_t>(t) * TOK + r0 - vis, nodes);
-                        // (kSplit: lanes 0..15 hold the rows' tokens 0..63, lanes 16..31 the others)
-                        const uint32_t group = kSplit ? 0xFFFFu << (16 * half) : 0xFFFFFFFFu;
-                        odd = __reduce_or_sync(group, odd);
-                        for (; odd; odd &= odd - 1) {
-                            const uint32_t at = st + (r0 + __ffs(odd) - 1) * 128 + (lane & 7) * 16;
-                            const uint4 w = finite_or_zero(ld_shared_v4(at));
-                            st_shared_v4(at, w.x, w.y, w.z, w.w);
-                        }
-                    }
-                }
-
                 float alpha = 1.f;
                 if (warp_real) {
                     const int32_t tok0 = static_cast<int32_t>(t) * TOK + TT * half;
-                    if constexpr (kTree) {
-                        if (!real_row || tok0 + TT > vis) {
-#pragma unroll
-                            for (int c = 0; c < TT / 32; ++c) {
-                                const int32_t d = tok0 + 32 * c - vis;
-                                const uint32_t bits = !real_row ? 0u
-                                                      : d <= -32 ? ~0u
-                                                                 : tree_bits(mask, args.mask_words, node, nodes, d);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    v[32 * c + j] = (bits >> j) & 1u ? v[32 * c + j] : -INFINITY;
-                            }
-                        }
-                    } else if (tok0 + TT > vis) {   // mask the tokens this row does not see
+                    if (tok0 + TT > vis) {   // mask the tokens this row does not see
 #pragma unroll
                         for (int j = 0; j < TT; ++j) v[j] = (tok0 + j < vis) ? v[j] : -INFINITY;
                     }
@@ -1814,7 +1750,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             }
             if (!ok) break;
             have = walk.next();
-            if (have) load_q(walk);
+            if (have) load_q(walk.seg_b);
             const int64_t kl = k - 1;
             if (!wait_bounded(bar(&misc->pv_done[kl & 1]), (kl >> 1) & 1, abort_flag,
                               args.timeout_ns))
@@ -1825,7 +1761,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                 // same sum in both lanes); each lane writes one 32-channel half
                 const float l_row = kSplit ? l_run + __shfl_xor_sync(0xffffffffu, l_run, 16) : l_run;
                 const float inv = (l_row > 0.f) ? 1.f / l_row : 0.f;
-                float *dst = args.o_part + (slot * (kTree ? ITEM_ROWS : args.rows) + row) * DC;
+                float *dst = args.o_part + (slot * args.rows + row) * DC;
 #pragma unroll 1
                 for (int cch = 0; cch < DC / 32; ++cch) {
                     uint32_t o[32];
@@ -1839,20 +1775,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                             o[j] = __float_as_uint(half ? other + mine : mine + other);   // lane order: tokens 0..63 first
                         }
                     }
-                    if (kTree && slot < 0) {   // the whole item: O / l is final, rounded to bf16
-                        if (real_row && (!kSplit || cch == half)) {
-                            uint4 *d8 = reinterpret_cast<uint4 *>(args.o_lat + (out_row0 + row) * DC + 32 * cch);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t h[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    h[i] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * i]) * inv,
-                                                       __uint_as_float(o[8 * j + 2 * i + 1]) * inv);
-                                d8[j] = make_uint4(h[0], h[1], h[2], h[3]);
-                            }
-                        }
-                    } else if (real_row && (!kSplit || cch == half)) {
+                    if (real_row && (!kSplit || cch == half)) {
                         float4 *d4 = reinterpret_cast<float4 *>(dst + 32 * cch);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
@@ -1862,13 +1785,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                                                 __uint_as_float(o[4 * j + 3]) * inv);
                     }
                 }
-                if (real_row && half == 0) {
-                    // (kTree: a NaN sum stays NaN, so that the merge of a shared item keeps it)
-                    const float lse =
-                        (kTree ? l_row != 0.f : l_row > 0.f) ? m_run * args.scale + logf(l_row) : -INFINITY;
-                    if (!kTree || slot >= 0) args.lse_part[slot * (kTree ? ITEM_ROWS : args.rows) + row] = lse;
-                    else if (args.lse_out) args.lse_out[out_row0 + row] = lse;
-                }
+                if (real_row && half == 0)
+                    args.lse_part[slot * args.rows + row] =
+                        (l_row > 0.f) ? m_run * args.scale + logf(l_row) : -INFINITY;
             }
             ptx::tc_fence_before();
             arrive(&misc->o_free);

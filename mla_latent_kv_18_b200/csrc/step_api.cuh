@@ -3,6 +3,7 @@
 #include "mla_step.h"
 #include "step_kernels.cuh"
 #include "tree_combine.cuh"
+#include "tree_single.cuh"
 
 namespace {
 
@@ -29,12 +30,12 @@ mla_status step_ready() {
         };
         const void *pair = reinterpret_cast<const void *>(mla::decode_pair_kernel<false, true>);
         const void *pair8 = reinterpret_cast<const void *>(mla::decode_pair_kernel<true, true>);
-        const void *one = reinterpret_cast<const void *>(mla::decode_single_kernel<false, true>);
-        const void *split = reinterpret_cast<const void *>(mla::decode_single_kernel<true, true>);
+        const void *one = reinterpret_cast<const void *>(mla::tree_single_kernel<false>);
+        const void *split = reinterpret_cast<const void *>(mla::tree_single_kernel<true>);
         const void *merge = reinterpret_cast<const void *>(mla::tree_combine_kernel);
         const void *plan = reinterpret_cast<const void *>(mla::step_plan_kernel);
         if (!big(pair, mla::pair::SMEM_BYTES) || !big(pair8, mla::pair::SMEM_BYTES) ||
-            !big(one, mla::single::SMEM_BYTES) || !big(split, mla::single::SMEM_BYTES) ||
+            !big(one, mla::tsingle::SMEM_BYTES) || !big(split, mla::tsingle::SMEM_BYTES) ||
             !big(plan, mla::plan_smem_bytes(mla::kPlanMaxBatch)) || !carve(pair) || !carve(pair8) || !carve(one) ||
             !carve(split) || !carve(merge))
             s.status = MLA_ERR_CUDA;
@@ -194,18 +195,21 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
                             mla::pair::SMEM_BYTES, s, m32, m64, mkr, mkr /* no scales */, mq, a);
         }
     } else {
-        // at most 64 query rows a sequence: each row on two TMEM lanes, half the tile's tokens each
-        const bool split = max_nodes * H <= 64;
+        // Items of 64 rows (each row on two TMEM lanes, half the tile's tokens each) take
+        // about half the time of items of 128, so they are taken where they cover the
+        // largest sequence's rows with less.
+        const int64_t most = static_cast<int64_t>(max_nodes) * H;
+        const bool split = (most + 63) / 64 < 2 * ((most + 127) / 128);
         c.tile_tokens = mla::single::TOK;
         c.item_rows = split ? 64 : 128;
         c.min_tiles = 1;
         CUtensorMap mc, mkr;
         if ((st = pool_map(&mc, ckv, 64, num_pages, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != MLA_OK) return st;
         if ((st = pool_map(&mkr, kr, 8, num_pages, 8, 64, CU_TENSOR_MAP_SWIZZLE_NONE)) != MLA_OK) return st;
-        st = split ? launch_pdl(mla::decode_single_kernel<true, true>, dim3(num_parts), dim3(mla::kDecodeThreads),
-                                mla::single::SMEM_BYTES, s, mc, mkr, a)
-                   : launch_pdl(mla::decode_single_kernel<false, true>, dim3(num_parts), dim3(mla::kDecodeThreads),
-                                mla::single::SMEM_BYTES, s, mc, mkr, a);
+        st = split ? launch_pdl(mla::tree_single_kernel<true>, dim3(num_parts), dim3(mla::tsingle::THREADS),
+                                mla::tsingle::SMEM_BYTES, s, mc, mkr, a)
+                   : launch_pdl(mla::tree_single_kernel<false>, dim3(num_parts), dim3(mla::tsingle::THREADS),
+                                mla::tsingle::SMEM_BYTES, s, mc, mkr, a);
     }
     if (st != MLA_OK || num_parts == 1) return st;   // one partition shares nothing
     const int32_t warps_per_row = dc <= 128 ? 1 : dc / 128;
