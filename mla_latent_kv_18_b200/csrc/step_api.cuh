@@ -200,9 +200,9 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
         // largest sequence's rows with less.
         const int64_t most = static_cast<int64_t>(max_nodes) * H;
         const bool split = (most + 63) / 64 < 2 * ((most + 127) / 128);
-        c.tile_tokens = mla::single::TOK;
+        c.tile_tokens = mla::tsingle::TOK;
         c.item_rows = split ? 64 : 128;
-        c.min_tiles = 1;
+        c.min_tiles = mla::tsingle::MIN_TILES;
         CUtensorMap mc, mkr;
         if ((st = pool_map(&mc, ckv, 64, num_pages, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != MLA_OK) return st;
         if ((st = pool_map(&mkr, kr, 8, num_pages, 8, 64, CU_TENSOR_MAP_SWIZZLE_NONE)) != MLA_OK) return st;
