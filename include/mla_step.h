@@ -162,7 +162,7 @@ mla_status mla_append_kv_slots_fp8(const mla_dims *dims, const void *ckv_new,
 /* Partitions mla_decode_tree should be given on a device with num_sms
  * multiprocessors (one per CTA pair for d_latent 512, one per CTA for 64), and the
  * bytes of workspace that num_parts partitions need: 2 num_parts slots of 128
- * query rows, whatever the batch. Host only; 0 for invalid arguments. */
+ * query rows and num_parts notes of 16 bytes, whatever the batch. Host only; 0 for invalid arguments. */
 int32_t mla_tree_num_parts(const mla_dims *dims, int32_t num_sms);
 size_t mla_tree_workspace_bytes(const mla_dims *dims, int32_t num_parts);
 

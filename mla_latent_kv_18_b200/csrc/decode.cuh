@@ -66,6 +66,7 @@ struct DecodeArgs {
     const uint32_t *masks;       // [total_tokens, mask_words] ancestor bits, or null (a chain)
     __nv_bfloat16 *o_lat;        // [total_tokens, H, d_c]
     float *lse_out;              // [total_tokens, H] or null
+    TreeShared *shared;          // [num_parts]: the item each partition leaves to be merged
     int32_t mask_words;
 };
 
@@ -645,7 +646,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                                      q_seq(walk));
             }
             bool first_seg = walk.primed;
+            [[maybe_unused]] TreeShared shared = {0, 0, 0, 0};
             for (; !*abort_flag && walk.next(); first_seg = false) {
+                if constexpr (kTree) shared = walk.shared();   // (only the last segment's can be one)
                 const int32_t *trow = args.block_table + static_cast<int64_t>(walk.seg_b) * args.max_pages;
                 for (int64_t t = walk.t_begin; t < walk.t_end; ++t, ++k) {
                     const int s = static_cast<int>(k % nst);
@@ -708,6 +711,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                     }
                 }
             }
+            if (kTree && qk && rank == 0) args.shared[part] = shared;
             if (bad_page) record_error(kErrDeviceBounds);
             // drain: the leader waits until every issued slot has landed
             // (E4M3: each CTA waits for its own code copies)

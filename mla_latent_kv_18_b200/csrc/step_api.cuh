@@ -159,19 +159,18 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
     a.mask_words = (max_nodes + 31) / 32;
     a.o_lat = static_cast<__nv_bfloat16 *>(o_lat);
     a.lse_out = lse_out;
+    a.shared = reinterpret_cast<mla::TreeShared *>(a.lse_part + slots * 128);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     mla::TreeCombineArgs c;
     c.o_part = a.o_part;
     c.lse_part = a.lse_part;
-    c.tree = a.tree;
+    c.shared = a.shared;
     c.o_lat = a.o_lat;
     c.lse_out = lse_out;
     c.d_c = dc;
     c.num_parts = num_parts;
     if (pair) {
-        c.tile_tokens = mla::pair::TOK;
         c.item_rows = mla::pair::TREE_ROWS;
-        c.min_tiles = mla::pair::TREE_MIN_TILES;
         CUtensorMap m32, m64, mkr, mq;
         if ((st = pool_map(&mkr, kr, 64, num_pages, 64, mla::pair::OWN, CU_TENSOR_MAP_SWIZZLE_128B)) != MLA_OK)
             return st;
@@ -195,14 +194,9 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
                             mla::pair::SMEM_BYTES, s, m32, m64, mkr, mkr /* no scales */, mq, a);
         }
     } else {
-        // Items of 64 rows (each row on two TMEM lanes, half the tile's tokens each) take
-        // about half the time of items of 128, so they are taken where they cover the
-        // largest sequence's rows with less.
-        const int64_t most = static_cast<int64_t>(max_nodes) * H;
-        const bool split = (most + 63) / 64 < 2 * ((most + 127) / 128);
-        c.tile_tokens = mla::tsingle::TOK;
+        // at most 64 query rows a sequence: each row on two TMEM lanes, half the tile's tokens each
+        const bool split = static_cast<int64_t>(max_nodes) * H <= 64;
         c.item_rows = split ? 64 : 128;
-        c.min_tiles = mla::tsingle::MIN_TILES;
         CUtensorMap mc, mkr;
         if ((st = pool_map(&mc, ckv, 64, num_pages, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != MLA_OK) return st;
         if ((st = pool_map(&mkr, kr, 8, num_pages, 8, 64, CU_TENSOR_MAP_SWIZZLE_NONE)) != MLA_OK) return st;
@@ -212,9 +206,10 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
                                 mla::tsingle::SMEM_BYTES, s, mc, mkr, a);
     }
     if (st != MLA_OK || num_parts == 1) return st;   // one partition shares nothing
-    const int32_t warps_per_row = dc <= 128 ? 1 : dc / 128;
-    const dim3 grid(num_parts - 1, (c.item_rows * warps_per_row + mla::kTreeCombineWarps - 1) / mla::kTreeCombineWarps);
-    return launch_pdl(mla::tree_combine_kernel, grid, dim3(32 * mla::kTreeCombineWarps), 0, s, c);
+    const int64_t units = static_cast<int64_t>(num_parts - 1) * c.item_rows * (dc <= 128 ? 1 : dc / 128);
+    const int64_t warps = mla::kTreeCombineThreads / 32;
+    const int64_t ctas = std::min<int64_t>((units + warps - 1) / warps, 2 * static_cast<int64_t>(device_sms()));
+    return launch_pdl(mla::tree_combine_kernel, dim3(static_cast<unsigned>(ctas)), dim3(mla::kTreeCombineThreads), 0, s, c);
 }
 
 template <typename T>
@@ -411,7 +406,8 @@ size_t mla_tree_workspace_bytes(const mla_dims *dims, int32_t num_parts) {
     mla_dims one = *dims;
     one.n_q = 1;
     if (check_dims(&one, true) != MLA_OK) return 0;
-    return static_cast<size_t>(2 * static_cast<int64_t>(num_parts) * 128 * (dims->d_latent + 1) * 4);
+    return static_cast<size_t>(2 * static_cast<int64_t>(num_parts) * 128 * (dims->d_latent + 1) * 4 +
+                               static_cast<int64_t>(num_parts) * sizeof(mla::TreeShared));
 }
 
 mla_status mla_decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, const mla_pool *ckv,

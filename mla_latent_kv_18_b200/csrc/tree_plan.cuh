@@ -15,8 +15,8 @@
 // Only a partition's first and last segment can belong to an item that is shared
 // with a neighbour, so a partition has two partial-result slots, 2 p for its first
 // segment and 2 p + 1 for a later one, whatever the batch: the workspace does not
-// grow with the number of query tokens. An item is merged by the partition that it
-// begins in.
+// grow with the number of query tokens. The partition that a shared item begins in
+// leaves a note of it (TreeShared) for the merge.
 #pragma once
 #include <cstdint>
 
@@ -54,17 +54,34 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeBatch &t, int32_t b, int32
     return q;
 }
 
+// A shared item, noted by the partition that it begins in (rows 0: none): its rows
+// in the output, the slot of its part there, and the last partition that has a part,
+// every later one in slot 2 p.
+struct TreeShared {
+    int32_t row0, rows, slot, last;
+};
+
 // Walks the items of one partition; every thread that walks it gets the same
 // segments. Costs fit 32 bits (checked on the host).
 struct TreeWalker {
     TreeBatch batch;
     int32_t tile_tokens, item_rows, part;
     int32_t tile, te;             // cost position reached, end of this partition's range
+    int32_t C, P;                 // total cost, partitions in use
     int32_t b, blk, O;            // the next item: sequence, row block, cost offset
     bool later;                   // a segment has been handed out
     bool primed;                  // the current segment was found ahead: next() hands it out
     // current segment
     int32_t seg_b, L, nodes, first_tok, row0, rows, t_begin, t_end, slot;   // slot < 0: the whole item
+    int32_t item_end;             // cost position after the item's last tile
+
+    // The current segment's note, if its item begins here and goes on.
+    __device__ TreeShared shared() const {
+        TreeShared s = {0, 0, 0, 0};
+        if (slot >= 0 && t_begin == 0)
+            s = {row0, rows, slot, static_cast<int32_t>(part_of_tile(item_end - 1, C, P))};
+        return s;
+    }
 
     __device__ bool next() {
         if (primed) {
@@ -89,6 +106,7 @@ struct TreeWalker {
             first_tok = q.first_tok;
             row0 = q.first_tok * batch.heads + i * item_rows;
             rows = min(item_rows, q.nodes * batch.heads - i * item_rows);
+            item_end = at + q.tiles;
             t_begin = max(tile - at, 0);
             t_end = min(te - at, q.tiles);
             slot = (t_begin == 0 && t_end == q.tiles) ? -1 : 2 * part + (later ? 1 : 0);
@@ -174,6 +192,8 @@ __device__ inline TreeWalker tree_start(const TreeBatch &t, int32_t part, int32_
     w.tile_tokens = tile_tokens;
     w.item_rows = item_rows;
     w.part = part;
+    w.C = p.C;
+    w.P = p.P;
     if (part < p.P) {
         w.tile = static_cast<int32_t>(part_start(part, p.C, p.P));
         w.te = static_cast<int32_t>(part_start(part + 1, p.C, p.P));

@@ -78,7 +78,7 @@ def test_tree_sizing(b):
     assert b.lib.mla_tree_num_parts(d, 148) == 74
     assert b.lib.mla_tree_num_parts(_dims(b, d_latent=64, d_rope=8, n_q=999), 148) == 148
     assert b.lib.mla_tree_num_parts(_dims(b, num_heads=129), 148) == 0
-    assert b.lib.mla_tree_workspace_bytes(d, 74) == 2 * 74 * 128 * 513 * 4
+    assert b.lib.mla_tree_workspace_bytes(d, 74) == 2 * 74 * 128 * 513 * 4 + 74 * 16
     assert b.lib.mla_tree_workspace_bytes(d, 0) == 0
 
 
