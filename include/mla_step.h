@@ -122,7 +122,8 @@ typedef struct {
  * y's, and with mscale 1 the way back. Rows with a negative position are skipped (their output is left as it was).
  * inv_freq [rot_dim / 2] fp64 and positions [num_tokens] int32 are device
  * pointers. rot_dim even, 2 <= rot_dim <= 4096, 0 <= offset, offset + rot_dim <= width <= 65536,
- * heads of both tensors together <= 65536; any strides (16-byte accesses are used where pointers,
+ * heads of both tensors together <= 65536, and heads * width <= 2^24
+ * (MLA_ERR_UNSUPPORTED beyond); any strides (16-byte accesses are used where pointers,
  * strides and widths are multiples of 16 bytes).
  */
 mla_status mla_rotary(const mla_rotary_tensor *x, const mla_rotary_tensor *y, int32_t dtype,

@@ -869,37 +869,51 @@ struct AppendArgs {
 
 // E4M3 with one fp32 scale per token: amax over the row, then
 // inv = 448 / amax, code = E4M3_rn_satfinite(x * inv), scale = amax / 448,
-// all with IEEE-rounded fp32 operations. The codes of one row of d_c bf16 go to
-// dst8; returns the scale. Warp-cooperative.
+// all with IEEE-rounded fp32 operations.
+__device__ __forceinline__ float amax_of8(const uint4 &v) {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
+    float amax = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float2 f = __bfloat1622float2(h[q]);
+        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+    return amax;
+}
+__device__ __forceinline__ uint2 quantise8_e4m3(const uint4 &v, float inv) {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
+    uint32_t w[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const float2 f0 = __bfloat1622float2(h[2 * q]), f1 = __bfloat1622float2(h[2 * q + 1]);
+        const uint32_t c0 = __nv_cvt_float_to_fp8(__fmul_rn(f0.x, inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t c1 = __nv_cvt_float_to_fp8(__fmul_rn(f0.y, inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t c2 = __nv_cvt_float_to_fp8(__fmul_rn(f1.x, inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t c3 = __nv_cvt_float_to_fp8(__fmul_rn(f1.y, inv), __NV_SATFINITE, __NV_E4M3);
+        w[q] = c0 | (c1 << 8) | (c2 << 16) | (c3 << 24);
+    }
+    return make_uint2(w[0], w[1]);
+}
+// The codes of one row of d_c bf16 to dst8; returns the scale. Warp-cooperative.
 __device__ __forceinline__ float quantise_row_e4m3(const uint4 *src, int32_t d_c, uint8_t *dst8, int lane) {
     float amax = 0.f;
-    for (int i = lane; i < d_c / 8; i += 32) {
-        const uint4 v = src[i];
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float2 f = __bfloat1622float2(h[q]);
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-    }
+    for (int i = lane; i < d_c / 8; i += 32) amax = fmaxf(amax, amax_of8(src[i]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 1.f;
-    for (int i = lane; i < d_c / 8; i += 32) {
-        const uint4 v = src[i];
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
-        uint32_t w[2];
+    for (int i = lane; i < d_c / 8; i += 32) *reinterpret_cast<uint2 *>(dst8 + 8 * i) = quantise8_e4m3(src[i], inv);
+    return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+}
+// The same of a row of at most 512 in registers: lane holds 16-byte pieces lane and lane + 32.
+__device__ __forceinline__ float quantise_row_e4m3(const uint4 (&v)[2], int32_t d_c, uint8_t *dst8, int lane) {
+    float amax = fmaxf(amax_of8(v[0]), amax_of8(v[1]));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const float2 f0 = __bfloat1622float2(h[2 * q]), f1 = __bfloat1622float2(h[2 * q + 1]);
-            const uint32_t c0 = __nv_cvt_float_to_fp8(__fmul_rn(f0.x, inv), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t c1 = __nv_cvt_float_to_fp8(__fmul_rn(f0.y, inv), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t c2 = __nv_cvt_float_to_fp8(__fmul_rn(f1.x, inv), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t c3 = __nv_cvt_float_to_fp8(__fmul_rn(f1.y, inv), __NV_SATFINITE, __NV_E4M3);
-            w[q] = c0 | (c1 << 8) | (c2 << 16) | (c3 << 24);
-        }
-        *reinterpret_cast<uint2 *>(dst8 + 8 * i) = make_uint2(w[0], w[1]);
-    }
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (lane + 32 * i < d_c / 8)
+            *reinterpret_cast<uint2 *>(dst8 + 8 * (lane + 32 * i)) = quantise8_e4m3(v[i], inv);
     return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
 }
 

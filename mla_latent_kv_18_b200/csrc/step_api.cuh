@@ -269,7 +269,8 @@ mla_status mla_step_plan(const int32_t *cached_lens, const int32_t *new_lens, in
     a.max_nodes = parents ? max_nodes : 0;
     a.words = parents ? (max_nodes + 31) / 32 : 0;
     const int64_t work = std::max<int64_t>(num_tokens, static_cast<int64_t>(batch) + 1);
-    const int64_t ctas = std::min<int64_t>((work + mla::kPlanThreads - 1) / mla::kPlanThreads, device_sms());
+    const int64_t ctas = std::min<int64_t>((work + mla::kPlanThreads - 1) / mla::kPlanThreads,
+                                           2 * static_cast<int64_t>(device_sms()));
     return launch_pdl(mla::step_plan_kernel, dim3(static_cast<unsigned>(std::max<int64_t>(ctas, 1))),
                       dim3(mla::kPlanThreads), mla::plan_smem_bytes(batch), static_cast<cudaStream_t>(stream), a);
 }
@@ -333,6 +334,7 @@ mla_status mla_rotary(const mla_rotary_tensor *x, const mla_rotary_tensor *y, in
         heads += t->heads;
     }
     if (heads > 65536) return MLA_ERR_INVALID_ARG;
+    if (heads * width > (1 << 24)) return MLA_ERR_UNSUPPORTED;
     if (num_tokens == 0 || heads == 0) return MLA_OK;
     if (!positions || !inv_freq || !aligned(positions, 4) || !aligned(inv_freq, 8)) return MLA_ERR_INVALID_ARG;
     mla_status st = step_ready();
@@ -345,27 +347,19 @@ mla_status mla_rotary(const mla_rotary_tensor *x, const mla_rotary_tensor *y, in
     a.width = width;
     a.offset = offset;
     a.half = half;
-    // Items of a head: pairs (or vectors of them), then what is copied. (Where one
-    // tensor is turned in place and the other is not, both copy: in place that
-    // rewrites the same values.)
+    // Places of a head. (Where one tensor is turned in place and the other is not, both
+    // copy: in place that rewrites the same values.)
     const int32_t e = vec ? E : 1;
     a.turned = !vec ? half : layout == MLA_ROPE_HALF ? half / e : rot_dim / e;
-    const int32_t per_head = a.turned + (copy ? (width - rot_dim) / e : 0);
-    // A CTA's share: about 2048 items, fewer heads where that leaves SMs idle, and more
-    // tokens where a token has few items, as long as its table fits.
-    const int64_t want = 2 * static_cast<int64_t>(device_sms());
-    int64_t hc = std::min<int64_t>(heads, std::max<int64_t>(1, 2048 / per_head));
-    int64_t tt = std::max<int64_t>(1, std::min<int64_t>(2048 / std::max<int64_t>(1, hc * per_head),
-                                                        mla::kRotaryMaxTable / half));
-    auto ctas = [&] { return ((num_tokens + tt - 1) / tt) * ((heads + hc - 1) / hc); };
-    while (tt > 1 && ctas() < want) tt = (tt + 1) / 2;
-    while (hc > 1 && hc * per_head > mla::kRotaryThreads && ctas() < want) hc = (hc + 1) / 2;
+    a.copied = copy ? (width - rot_dim) / e : 0;
+    const int64_t places = heads * (static_cast<int64_t>(a.turned) + a.copied);
+    const int64_t across = (places + mla::kRotaryThreads - 1) / mla::kRotaryThreads;   // <= 65536
+    if (across > 65535) return MLA_ERR_UNSUPPORTED;
+    // Tokens of a CTA: 32, while their table fits and eight CTAs per SM are left.
+    int64_t tt = std::min<int64_t>(32, mla::kRotaryMaxTable / half);
+    while (tt > 1 && (num_tokens + tt - 1) / tt * across < 8 * static_cast<int64_t>(device_sms())) tt /= 2;
     a.TT = static_cast<int32_t>(tt);
-    a.HC = static_cast<int32_t>(hc);
-    a.per_head.set(static_cast<uint32_t>(per_head));
-    a.per_token.set(static_cast<uint32_t>(hc));
-    const dim3 grid(static_cast<unsigned>((num_tokens + tt - 1) / tt), static_cast<unsigned>((heads + hc - 1) / hc));
-    if (grid.y > 65535) return MLA_ERR_UNSUPPORTED;
+    const dim3 grid(static_cast<unsigned>((num_tokens + tt - 1) / tt), static_cast<unsigned>(across));
     const uint32_t smem = static_cast<uint32_t>(tt * half * sizeof(float2));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool h = layout == MLA_ROPE_HALF;

@@ -9,6 +9,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/CUDAContextLight.h>
+#include <ATen/ops/as_strided_native.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -182,11 +183,12 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t) {
         if (none(a[8])) {
             // the int32 ones share an allocation
             const at::Tensor all = empty({2 * B + 2 + 2 * T + T * words}, at::kInt, index);
-            int64_t at = 0;
+            int64_t first = 0;
             for (int i : {0, 1, 2, 3, 5, 6}) {
                 if (i == 6 && !tree) break;
-                o[i] = i == 6 ? all.as_strided({T, words}, {words, 1}, at) : all.as_strided({sizes[i]}, {1}, at);
-                at += sizes[i];
+                o[i] = i == 6 ? at::native::as_strided_tensorimpl(all, {T, words}, {words, 1}, first)
+                              : at::native::as_strided_tensorimpl(all, {sizes[i]}, {1}, first);
+                first += sizes[i];
             }
             o[4] = empty({T}, at::kLong, index);
         } else {

@@ -119,6 +119,10 @@ def test_rotary_refusals(b, kw):
     assert _rot(b, **kw) == INVALID
 
 
+def test_rotary_refuses_rows_too_wide(b):
+    assert _rot(b, heads=1024, width=32768, rot=64) == UNSUPPORTED
+
+
 def test_rotary_nothing_to_do_is_ok(b):
     assert _rot(b, T=0) == 0 and _rot(b, heads=0) == 0
 
