@@ -256,7 +256,8 @@ constexpr uint32_t OFF_FIRST_PAGES = OFF_EPI;
 constexpr uint32_t OFF_FIRST_WALKER = OFF_EPI + 64;   // kTree: the walker at its first segment (every role
                                                       // has copied it before a segment can end)
 constexpr int TREE_ROWS = 2 * ROWS_CTA;               // kTree: query rows per item
-constexpr int TREE_MIN_TILES = 8;                     // kTree: as the partition count of whole sequences
+constexpr int TREE_MIN_TILES = 4;                     // kTree: see tree_find
+constexpr int TREE_WHOLE = 10;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TMEM_O = 0;                 // two 128-column accumulators (c = 0, 1)
 constexpr uint32_t TMEM_S = 256;               // three 32-column score buffers
@@ -518,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
     if (kTree && warp == 0) {
         if constexpr (kTree) {
             TreeWalker w0 = tree_start(args.tree, static_cast<int32_t>(part), args.num_parts, TOK, TREE_ROWS,
-                                       TREE_MIN_TILES);
+                                       TREE_MIN_TILES, TREE_WHOLE);
             w0.primed = w0.next();
             if (lane == 0) {
                 *reinterpret_cast<TreeWalker *>(smem + OFF_FIRST_WALKER) = w0;

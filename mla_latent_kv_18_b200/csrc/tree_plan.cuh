@@ -124,10 +124,14 @@ struct TreePlan {
 };
 
 // Warp-cooperative: the plan's totals and the first item that ends after cost
-// position start(part), if part < P. min_tiles: the fewest tiles worth a partition
-// of their own. All 32 lanes must call it; every lane gets the result.
+// position start(part), if part < P. All 32 lanes must call it; every lane gets the
+// result. Fewer partitions than num_parts are used where there is little to do: items of
+// up to `whole` tiles on average are not split (a merge costs as much as some tiles: 8
+// one-item sequences of 512 tokens take 17.3 us whole and 19.9 us in halves), longer
+// ones into parts of `min_tiles` at least (one item of 1024 tokens: 18.6 us in parts of 8
+// tiles, 15.1 us of 4; of 4096: 21.2, 20.0, and 23.2 us of 2).
 __device__ inline TreePlan tree_find(const TreeBatch &t, int32_t part, int32_t num_parts, int32_t tile_tokens,
-                                     int32_t item_rows, int32_t min_tiles) {
+                                     int32_t item_rows, int32_t min_tiles, int32_t whole) {
     const int lane = threadIdx.x & 31;
     const int32_t W = switch_cost(tile_tokens);
     bool bad = false;
@@ -145,7 +149,7 @@ __device__ inline TreePlan tree_find(const TreeBatch &t, int32_t part, int32_t n
     TreePlan r = {0, 0, t.batch, 0, 0};
     if (items == 0) return r;
     r.C = N + W * (items - 1);
-    r.P = min(num_parts, (N + min_tiles - 1) / min_tiles);
+    r.P = min(num_parts, N > whole * items ? N / min_tiles : items);
     if (part >= r.P) return r;
     const int32_t ts = static_cast<int32_t>(part_start(part, r.C, r.P));
     int32_t CO = 0;
@@ -185,8 +189,8 @@ __device__ inline TreePlan tree_find(const TreeBatch &t, int32_t part, int32_t n
 
 // The walker of partition `part`, before its first segment (warp-cooperative).
 __device__ inline TreeWalker tree_start(const TreeBatch &t, int32_t part, int32_t num_parts, int32_t tile_tokens,
-                                        int32_t item_rows, int32_t min_tiles) {
-    const TreePlan p = tree_find(t, part, num_parts, tile_tokens, item_rows, min_tiles);
+                                        int32_t item_rows, int32_t min_tiles, int32_t whole) {
+    const TreePlan p = tree_find(t, part, num_parts, tile_tokens, item_rows, min_tiles, whole);
     TreeWalker w = {};
     w.batch = t;
     w.tile_tokens = tile_tokens;

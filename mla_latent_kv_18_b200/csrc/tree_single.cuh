@@ -38,6 +38,7 @@ using single::TOK;
 constexpr int THREADS = 352;                              // TMA, QK^T, 2 x 4 softmax, P.V warps
 constexpr int STAGES = 8;                                 // KV ring depth
 constexpr int NSB = 3;                                    // score buffers
+constexpr int MIN_TILES = 2, WHOLE = 4;                   // see tree_find
 constexpr uint32_t OFF_Q = 0;
 constexpr uint32_t OFF_STAGE = 20480;
 constexpr uint32_t OFF_MISC = OFF_STAGE + STAGES * STAGE_BYTES;
@@ -108,7 +109,8 @@ __global__ void __launch_bounds__(tsingle::THREADS, 1)
     }
     ptx::grid_dep_launch();
     if (warp == 0) {   // the plan reads only lengths, which the kernel ahead does not write
-        TreeWalker w0 = tree_start(args.tree, static_cast<int32_t>(blockIdx.x), args.num_parts, TOK, ITEM_ROWS, 1);
+        TreeWalker w0 = tree_start(args.tree, static_cast<int32_t>(blockIdx.x), args.num_parts, TOK, ITEM_ROWS, MIN_TILES,
+                                   WHOLE);
         w0.primed = w0.next();
         if (lane == 0) {
             misc->first = w0;
