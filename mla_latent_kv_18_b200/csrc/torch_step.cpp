@@ -9,7 +9,6 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/CUDAContextLight.h>
-#include <ATen/ops/as_strided_native.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -140,6 +139,15 @@ at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, int index) {
     return at::empty(sizes, at::TensorOptions(at::Device(at::kCUDA, index)).dtype(type));
 }
 
+// A contiguous tensor of `type` inside the allocation of a byte tensor, `first` elements in.
+at::Tensor piece(const at::Tensor &bytes, at::ScalarType type, int64_t first, at::IntArrayRef sizes) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(bytes.storage()), bytes.key_set(),
+                                                            c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_storage_offset(first);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+    return t;
+}
+
 struct Pools {
     mla_pool ckv, kr;
     int32_t pages;
@@ -181,16 +189,15 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t) {
         at::Tensor o[7];   // seq_lens, cu_tokens, seq_ids, positions, slots, free_head, masks
         const int64_t sizes[7] = {B, B + 1, T, T, T, 1, T * words};
         if (none(a[8])) {
-            // the int32 ones share an allocation
-            const at::Tensor all = empty({2 * B + 2 + 2 * T + T * words}, at::kInt, index);
-            int64_t first = 0;
-            for (int i : {0, 1, 2, 3, 5, 6}) {
-                if (i == 6 && !tree) break;
-                o[i] = i == 6 ? at::native::as_strided_tensorimpl(all, {T, words}, {words, 1}, first)
-                              : at::native::as_strided_tensorimpl(all, {sizes[i]}, {1}, first);
+            // one allocation: slots (int64) first, then the int32 ones
+            const at::Tensor all = empty({8 * T + 4 * (2 * B + 2 + 2 * T + T * words)}, at::kByte, index);
+            o[4] = piece(all, at::kLong, 0, {T});
+            int64_t first = 2 * T;
+            for (int i : {0, 1, 2, 3, 5}) {
+                o[i] = piece(all, at::kInt, first, {sizes[i]});
                 first += sizes[i];
             }
-            o[4] = empty({T}, at::kLong, index);
+            if (tree) o[6] = piece(all, at::kInt, first, {T, words});
         } else {
             require(PyTuple_Check(a[8]) && PyTuple_GET_SIZE(a[8]) == 7, call, "out is a StepPlan");
             for (int i = 0; i < 7; ++i) {
