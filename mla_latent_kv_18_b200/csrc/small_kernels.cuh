@@ -886,11 +886,11 @@ __device__ __forceinline__ uint2 quantise8_e4m3(const uint4 &v, float inv) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const float2 f0 = __bfloat1622float2(h[2 * q]), f1 = __bfloat1622float2(h[2 * q + 1]);
-        const uint32_t c0 = __nv_cvt_float_to_fp8(__fmul_rn(f0.x, inv), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t c1 = __nv_cvt_float_to_fp8(__fmul_rn(f0.y, inv), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t c2 = __nv_cvt_float_to_fp8(__fmul_rn(f1.x, inv), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t c3 = __nv_cvt_float_to_fp8(__fmul_rn(f1.y, inv), __NV_SATFINITE, __NV_E4M3);
-        w[q] = c0 | (c1 << 8) | (c2 << 16) | (c3 << 24);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(f0.x, inv), __fmul_rn(f0.y, inv)),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(f1.x, inv), __fmul_rn(f1.y, inv)),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        w[q] = lo | (hi << 16);
     }
     return make_uint2(w[0], w[1]);
 }

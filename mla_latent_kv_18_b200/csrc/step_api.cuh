@@ -355,8 +355,8 @@ mla_status mla_rotary(const mla_rotary_tensor *x, const mla_rotary_tensor *y, in
     const int64_t places = heads * (static_cast<int64_t>(a.turned) + a.copied);
     const int64_t across = (places + mla::kRotaryThreads - 1) / mla::kRotaryThreads;   // <= 65536
     if (across > 65535) return MLA_ERR_UNSUPPORTED;
-    // Tokens of a CTA: 32, while their table fits and eight CTAs per SM are left.
-    int64_t tt = std::min<int64_t>(32, mla::kRotaryMaxTable / half);
+    // Tokens of a CTA: 16, while their table fits and eight CTAs per SM are left.
+    int64_t tt = std::min<int64_t>(16, mla::kRotaryMaxTable / half);
     while (tt > 1 && (num_tokens + tt - 1) / tt * across < 8 * static_cast<int64_t>(device_sms())) tt /= 2;
     a.TT = static_cast<int32_t>(tt);
     const dim3 grid(static_cast<unsigned>((num_tokens + tt - 1) / tt), static_cast<unsigned>(across));

@@ -249,9 +249,9 @@ struct Elem<float> {
 // layout one of each half; where strides or widths do not allow that (kVec), a pair or a
 // channel) and walks TT tokens with it, the loads of four of them in flight, so no index is
 // divided in the loop; a CTA's 256 places share the TT * rot / 2 cosines and sines, made while
-// the first loads are on their way. Places that turn come before places that copy.
+// the first loads are on their way.
 // Bound by HBM for prompts (every byte once in and once out), by latency for a
-// step's tokens. 16384 tokens x 129 heads of 192, 64 of them turned: 300 us, 5.4 TB/s.
+// step's tokens. 16384 tokens x 129 heads of 192, 64 of them turned: 288 us, 5.6 TB/s (253 us interleaved).
 // ---------------------------------------------------------------------------
 struct RotaryTensor {
     const void *in;
@@ -276,7 +276,7 @@ constexpr int kRotaryMaxTokens = 32;    // tokens of a CTA
 constexpr int kRotaryFlight = 4;
 
 template <typename T, bool kHalf, bool kVec>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kRotaryThreads, kVec && !kHalf ? 5 : 3) rotary_kernel(const RotaryArgs a) {
     extern __shared__ float2 rotary_cs[];
     __shared__ int32_t s_pos[kRotaryMaxTokens];
     constexpr int E = kVec ? 16 / static_cast<int>(sizeof(T)) : 1;
@@ -287,23 +287,18 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
     };
     const int32_t t0 = blockIdx.x * a.TT, nt = min(a.TT, a.tokens - t0);
     // this thread's place: head h of both tensors' and channel c
-    const int32_t heads = a.heads[0] + a.heads[1];
-    int32_t n = blockIdx.y * kRotaryThreads + threadIdx.x, h = 0, item = 0, c = 0;
-    const bool turns = n < heads * a.turned;
-    bool active = true;
-    if (turns) {
-        h = n / a.turned;
-        item = n - h * a.turned;
-        c = a.offset + item * (kHalf || kVec ? E : 2);
-    } else {
-        n -= heads * a.turned;
-        active = n < heads * a.copied;
-        if (active) {
-            h = n / a.copied;
-            c = (n - h * a.copied) * E;
-            if (c >= a.offset) c += 2 * a.half;
-        }
-    }
+    const int32_t n = blockIdx.y * kRotaryThreads + threadIdx.x, per_head = a.turned + a.copied;
+    int32_t h = n / per_head;
+    const int32_t place = n - h * per_head;
+    const bool active = h < a.heads[0] + a.heads[1];
+    if (!active) h = 0;
+    // copied channels before the turned ones, those, and the copied ones after
+    const int32_t before = a.copied ? a.offset / E : 0;
+    const bool turns = place >= before && place < before + a.turned;
+    const int32_t item = place - before;
+    const int32_t c = turns            ? a.offset + item * (kHalf || kVec ? E : 2)
+                      : place < before ? place * E
+                                       : a.offset + 2 * a.half + (item - a.turned) * E;
     const int w = h >= a.heads[0] ? 1 : 0;
     const RotaryTensor &x = a.x[w];
     h -= w ? a.heads[0] : 0;
