@@ -258,6 +258,11 @@ constexpr uint32_t OFF_FIRST_WALKER = OFF_EPI + 64;   // kTree: the walker at it
 constexpr int TREE_ROWS = 2 * ROWS_CTA;               // kTree: query rows per item
 constexpr int TREE_MIN_TILES = 4;                     // kTree: see tree_find
 constexpr int TREE_WHOLE = 10;
+// kTree: cost of a switch in tiles, measured: 16 ragged sequences of up to 4096 tokens,
+// 4 nodes, bf16 cache 42.0 us with 8, 39.8 with 6, 44.8 with 14 (16 equal ones with 8 nodes:
+// 155.0, 155.4, 154.7); E4M3 cache, whose tiles take longer, 65.1 us with 8, 59.9 with 5,
+// 70.2 with 14.
+constexpr int TREE_GAP = 6, TREE_GAP_FP8 = 5;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TMEM_O = 0;                 // two 128-column accumulators (c = 0, 1)
 constexpr uint32_t TMEM_S = 256;               // three 32-column score buffers

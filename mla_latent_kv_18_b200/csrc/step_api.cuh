@@ -154,7 +154,8 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
     a.heads = H;
     a.scale = scale_of(&one);
     a.scale_log2 = a.scale * 1.4426950408889634f;
-    a.tree = {seq_lens, cu_tokens, batch, max_pages, H, num_tokens, max_nodes};
+    a.tree = {seq_lens, cu_tokens, batch, max_pages, H, num_tokens, max_nodes,
+              !pair ? mla::tsingle::GAP : ckv8 ? mla::pair::TREE_GAP_FP8 : mla::pair::TREE_GAP};
     a.masks = masks;
     a.mask_words = (max_nodes + 31) / 32;
     a.o_lat = static_cast<__nv_bfloat16 *>(o_lat);

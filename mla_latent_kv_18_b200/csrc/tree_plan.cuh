@@ -4,9 +4,9 @@
 // Query tokens are packed: sequence b owns tokens cu_tokens[b] .. cu_tokens[b + 1)
 // of q, its n_b newest cache entries. Its n_b H query rows (token-major, head
 // minor) are cut into blocks of `item_rows`; a block against the sequence's
-// cache tiles is one item. All items lie end to end on a cost axis with W =
-// switch_cost(tile) virtual tiles between consecutive ones (the Q load and the
-// result write of a switch), and partition p of P owns the positions
+// cache tiles is one item. All items lie end to end on a cost axis with `gap`
+// virtual tiles between consecutive ones (the Q load and the result write of a
+// switch; fewer where a tile takes longer), and partition p of P owns the positions
 // [p C / P, (p + 1) C / P), as in the plan of whole sequences (common.cuh). Blocks
 // of one sequence are neighbours, so the partitions that work on them at the same
 // time find its cache in L2.
@@ -28,6 +28,7 @@ struct TreeBatch {
     const int32_t *seq_lens;    // [batch], the step's own tokens included
     const int32_t *cu_tokens;   // [batch + 1]
     int32_t batch, max_pages, heads, total_tokens, max_nodes;
+    int32_t gap;                // cost of a switch, in tiles
 };
 
 // What sequence b asks for; a bad one (a length outside the table, more query
@@ -97,7 +98,7 @@ struct TreeWalker {
                 continue;
             }
             const int32_t at = O, i = blk;
-            O += q.tiles + switch_cost(tile_tokens);
+            O += q.tiles + batch.gap;
             ++blk;
             if (at + q.tiles <= tile) continue;   // the partition starts in the gap after it
             seg_b = b;
@@ -133,7 +134,7 @@ struct TreePlan {
 __device__ inline TreePlan tree_find(const TreeBatch &t, int32_t part, int32_t num_parts, int32_t tile_tokens,
                                      int32_t item_rows, int32_t min_tiles, int32_t whole) {
     const int lane = threadIdx.x & 31;
-    const int32_t W = switch_cost(tile_tokens);
+    const int32_t W = t.gap;
     bool bad = false;
     int32_t N = 0, items = 0;
     TreeSeq first = {};   // this lane's sequence of the first 32, kept for the second pass

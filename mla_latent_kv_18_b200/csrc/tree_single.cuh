@@ -39,6 +39,7 @@ constexpr int THREADS = 352;                              // TMA, QK^T, 2 x 4 so
 constexpr int STAGES = 8;                                 // KV ring depth
 constexpr int NSB = 3;                                    // score buffers
 constexpr int MIN_TILES = 2, WHOLE = 4;                   // see tree_find
+constexpr int GAP = 3;                                    // cost of a switch, in tiles
 constexpr uint32_t OFF_Q = 0;
 constexpr uint32_t OFF_STAGE = 20480;
 constexpr uint32_t OFF_MISC = OFF_STAGE + STAGES * STAGE_BYTES;
