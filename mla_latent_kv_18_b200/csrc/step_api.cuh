@@ -162,6 +162,18 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
     a.lse_out = lse_out;
     a.shared = reinterpret_cast<mla::TreeShared *>(a.lse_part + slots * 128);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // The most items that these sizes can hold, and so the most partitions that the plan
+    // can use: a small step launches no more (one request of 320 tokens: 13.8 us with a full
+    // grid, 11.2 us with the partitions it can use).
+    const int64_t most = static_cast<int64_t>(max_nodes) * H;   // rows of a sequence
+    auto bound_items = [&](int64_t item_rows) {
+        return std::min(rows / item_rows + batch, batch * ((most + item_rows - 1) / item_rows));
+    };
+    auto bound_parts = [&](int64_t items, int64_t tile_tokens, int64_t min_tiles) {
+        const int64_t tiles = (static_cast<int64_t>(max_pages) * 64 + tile_tokens - 1) / tile_tokens;
+        a.num_parts = static_cast<int32_t>(std::min<int64_t>(num_parts, std::max(items, items * tiles / min_tiles)));
+    };
+    int64_t items;
     mla::TreeCombineArgs c;
     c.o_part = a.o_part;
     c.lse_part = a.lse_part;
@@ -169,9 +181,10 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
     c.o_lat = a.o_lat;
     c.lse_out = lse_out;
     c.d_c = dc;
-    c.num_parts = num_parts;
     if (pair) {
         c.item_rows = mla::pair::TREE_ROWS;
+        items = bound_items(c.item_rows);
+        bound_parts(items, mla::pair::TOK, mla::pair::TREE_MIN_TILES);
         CUtensorMap m32, m64, mkr, mq;
         if ((st = pool_map(&mkr, kr, 64, num_pages, 64, mla::pair::OWN, CU_TENSOR_MAP_SWIZZLE_128B)) != MLA_OK)
             return st;
@@ -184,30 +197,33 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
             CUtensorMap msc;
             if ((st = code_pool_map(&m32, ckv8, 512, num_pages, 128, mla::pair::OWN)) != MLA_OK) return st;
             if ((st = scale_map(&msc, scales, num_pages, 32)) != MLA_OK) return st;
-            st = launch_pdl(mla::decode_pair_kernel<true, true>, dim3(2 * num_parts), dim3(mla::kPairThreadsFp8),
+            st = launch_pdl(mla::decode_pair_kernel<true, true>, dim3(2 * a.num_parts), dim3(mla::kPairThreadsFp8),
                             mla::pair::SMEM_BYTES, s, m32, m32, mkr, msc, mq, a);
         } else {
             if ((st = pool_map(&m32, ckv, 512, num_pages, 64, mla::pair::OWN, CU_TENSOR_MAP_SWIZZLE_128B)) != MLA_OK)
                 return st;
             if ((st = pool_map(&m64, ckv, 512, num_pages, 64, mla::pair::TOK, CU_TENSOR_MAP_SWIZZLE_128B)) != MLA_OK)
                 return st;
-            st = launch_pdl(mla::decode_pair_kernel<false, true>, dim3(2 * num_parts), dim3(mla::kPairThreads),
+            st = launch_pdl(mla::decode_pair_kernel<false, true>, dim3(2 * a.num_parts), dim3(mla::kPairThreads),
                             mla::pair::SMEM_BYTES, s, m32, m64, mkr, mkr /* no scales */, mq, a);
         }
     } else {
         // at most 64 query rows a sequence: each row on two TMEM lanes, half the tile's tokens each
-        const bool split = static_cast<int64_t>(max_nodes) * H <= 64;
+        const bool split = most <= 64;
         c.item_rows = split ? 64 : 128;
+        items = bound_items(c.item_rows);
+        bound_parts(items, mla::single::TOK, mla::tsingle::MIN_TILES);
         CUtensorMap mc, mkr;
         if ((st = pool_map(&mc, ckv, 64, num_pages, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != MLA_OK) return st;
         if ((st = pool_map(&mkr, kr, 8, num_pages, 8, 64, CU_TENSOR_MAP_SWIZZLE_NONE)) != MLA_OK) return st;
-        st = split ? launch_pdl(mla::tree_single_kernel<true>, dim3(num_parts), dim3(mla::tsingle::THREADS),
+        st = split ? launch_pdl(mla::tree_single_kernel<true>, dim3(a.num_parts), dim3(mla::tsingle::THREADS),
                                 mla::tsingle::SMEM_BYTES, s, mc, mkr, a)
-                   : launch_pdl(mla::tree_single_kernel<false>, dim3(num_parts), dim3(mla::tsingle::THREADS),
+                   : launch_pdl(mla::tree_single_kernel<false>, dim3(a.num_parts), dim3(mla::tsingle::THREADS),
                                 mla::tsingle::SMEM_BYTES, s, mc, mkr, a);
     }
-    if (st != MLA_OK || num_parts == 1) return st;   // one partition shares nothing
-    const int64_t units = static_cast<int64_t>(num_parts - 1) * c.item_rows * (dc <= 128 ? 1 : dc / 128);
+    if (st != MLA_OK || a.num_parts == 1) return st;   // one partition shares nothing
+    c.num_parts = a.num_parts;
+    const int64_t units = std::min<int64_t>(a.num_parts - 1, items) * c.item_rows * (dc <= 128 ? 1 : dc / 128);
     const int64_t warps = mla::kTreeCombineThreads / 32;
     const int64_t ctas = std::min<int64_t>((units + warps - 1) / warps, 2 * static_cast<int64_t>(device_sms()));
     return launch_pdl(mla::tree_combine_kernel, dim3(static_cast<unsigned>(ctas)), dim3(mla::kTreeCombineThreads), 0, s, c);
