@@ -39,7 +39,8 @@
  *     for that kernel to finish before it reads that kernel's outputs. The
  *     decode calls read seq_lens and block_table before that wait, the
  *     combine calls seq_lens; the other calls read only their weights before
- *     it. The kernels of this library never write those inputs, so a stream
+ *     it. The only kernel of this library that writes those inputs is
+ *     mla_step_plan's (mla_step.h), which never lets the next one start early, so a stream
  *     that produces them with copies, with this library's calls or with
  *     kernels that do not trigger their dependents early is always safe; a
  *     custom kernel that triggers early (griddepcontrol.launch_dependents)

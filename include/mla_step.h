@@ -12,7 +12,9 @@
  * The conventions of mla_decode.h hold for every call: device pointers unless a
  * parameter says "host", nothing allocated, asynchronous on `stream`, argument
  * errors returned before anything is launched, data errors in the device error
- * word, deterministic results.
+ * word, deterministic results. mla_decode_tree reads seq_lens, cu_tokens and
+ * block_table before its dependency wait, as the decode calls do: a custom kernel that
+ * lets its dependents start early must not write them directly before it.
  *
  * Packed tokens: the step's query tokens lie sequence after sequence; sequence b
  * owns rows cu_tokens[b] .. cu_tokens[b + 1) of every per-token tensor, its newest
@@ -102,7 +104,8 @@ typedef enum {
 
 /* One [tokens, heads, width] tensor (host struct): element (t, h, c) is at
  * in[t * in_token + h * in_head + c], and the result's at out[...] likewise
- * (strides in elements; the channels of a head are contiguous). out == in with the same strides
+ * (strides in elements; the channels of a head are contiguous; in strides may be
+ * 0, out strides of more than one token or head may not). out == in with the same strides
  * turns in place; otherwise the two must not overlap. */
 typedef struct {
     const void *in;
@@ -191,9 +194,10 @@ size_t mla_tree_workspace_bytes(const mla_dims *dims, int32_t num_parts);
  * dims->n_q is ignored; num_heads <= 128. A sequence whose length does not fit its
  * table row, or with more tokens than max_nodes, than its length or than q has
  * rows, is skipped and sets MLA_ERR_DEVICE_BOUNDS, as a page id outside
- * [0, num_pages) does. Deterministic for a given num_parts.
- * num_tokens * num_heads and the plan's cost must stay below 2^31 (MLA_ERR_UNSUPPORTED):
- * (num_tokens * num_heads / 64 + batch) * (max_pages_per_seq + 16).
+ * [0, num_pages) does; a step whose sequences hold more than num_tokens tokens together
+ * (a cu_tokens that turns back) is skipped as a whole. Deterministic for a given num_parts.
+ * num_tokens * num_heads and the plan's cost must stay below 2^31, max_pages_per_seq below
+ * 2^25 - 1 (MLA_ERR_UNSUPPORTED): (num_tokens * num_heads / 64 + batch) * (max_pages_per_seq + 16).
  */
 mla_status mla_decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens,
                            const mla_pool *ckv, const mla_pool *kr, int32_t num_pages,

@@ -476,13 +476,21 @@ def attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, w_uk, w_uv, scale
 # ----------------------------------------------------------------------------
 # a step with any number of query tokens per sequence (include/mla_step.h). The
 # calls' checks, output allocation and launches are compiled (csrc/torch_step.cpp):
-# they run on their tensors' device and its current stream, or on `stream`.
+# they run on their tensors' device and its current stream, or on `stream`, a stream of
+# that device. Their outputs take no part in autograd.
 # ----------------------------------------------------------------------------
 
 TREE_MAX_NODES = 256
 STEP_MAX_BATCH = 16384
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _step.types(_b.MLAError, _b.MLADims)
+
+
+def _on(stream, tensor):
+    """`stream` made current, for tensors of its device."""
+    if stream.device != tensor.device:
+        raise _b.MLAError(1, f"stream of {stream.device}, tensors on {tensor.device}")
+    return torch.cuda.stream(stream)
 
 
 class StepPlan(NamedTuple):
@@ -522,7 +530,7 @@ def step_plan(cached_lens, new_lens, free_pages, free_head, block_table, num_tok
     parents [num_tokens] int32: index within the request of the drafted token each token follows
     (an earlier one; negative: it follows the context); max_nodes bounds new_lens then."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, block_table):
             return step_plan(cached_lens, new_lens, free_pages, free_head, block_table, num_tokens, parents, max_nodes,
                              out)
     return StepPlan._make(_step.plan(cached_lens, new_lens, free_pages, free_head, block_table, num_tokens, parents,
@@ -553,7 +561,7 @@ def rotary(x, positions, inv_freq, mscale=1.0, layout="interleaved", offset=0, i
     allocated here). inverse turns back: the gradient of x, given y's. k, a second tensor with heads of its
     own (and k_out), goes with it in the same launch. Returns out, or (out, k_out)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return rotary(x, positions, inv_freq, mscale, layout, offset, inverse, out, k, k_out)
     return _step.rotary(x, positions, inv_freq, mscale, layout, offset, inverse, out, k, k_out)
 
@@ -565,7 +573,7 @@ def append_kv_slots(ckv_new, kr_new, slots, ckv_pool, kr_pool, dims, positions=N
     (views of one projection). With positions [T] (and rope_frequencies' inv_freq, mscale) k_R is
     turned on the way, else copied."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, ckv_new):
             return append_kv_slots(ckv_new, kr_new, slots, ckv_pool, kr_pool, dims, positions, inv_freq, mscale, layout)
     _step.append(ckv_new, kr_new, slots, ckv_pool, None, kr_pool, dims, positions, inv_freq, mscale, layout)
 
@@ -576,7 +584,7 @@ def append_kv_slots_fp8(ckv_new, kr_new, slots, ckv8_pool, scales, kr_pool, dims
     if scales is None:
         raise _b.MLAError(1, "append_kv_slots_fp8: scales [pages, 64]")
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, ckv_new):
             return append_kv_slots_fp8(ckv_new, kr_new, slots, ckv8_pool, scales, kr_pool, dims, positions, inv_freq,
                                        mscale, layout)
     _step.append(ckv_new, kr_new, slots, ckv8_pool, scales, kr_pool, dims, positions, inv_freq, mscale, layout)
@@ -604,7 +612,7 @@ def decode_tree(q, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, dims, ma
     (o_lat [T, H, d_c] bf16, lse [T, H]); rows behind the last sequence are left as they were. Nothing is
     read back from the device. workspace: alloc_tree_workspace's; one is allocated if None."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return decode_tree(q, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks, num_parts,
                                workspace, o_lat, lse_out)
     return _step.tree(q, ckv_pool, None, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks, num_parts,
@@ -617,7 +625,7 @@ def decode_tree_fp8(q, ckv8_pool, scales, kr_pool, block_table, seq_lens, cu_tok
     if scales is None:
         raise _b.MLAError(1, "decode_tree_fp8: scales [pages, 64]")
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return decode_tree_fp8(q, ckv8_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes,
                                    masks, num_parts, workspace, o_lat, lse_out)
     return _step.tree(q, ckv8_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks, num_parts,
@@ -629,8 +637,14 @@ def tree_attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, w
     """One attention step of packed query tokens q_c [T, H, d_n], q_r [T, H, d_R] (turned) over the
     cache they are already in: absorb_q, decode_tree (over the E4M3 cache if its scales are given),
     absorb_out. Returns (out [T, H, d_v], lse [T, H])."""
-    if stream is not None or q_c.device.index != torch.cuda.current_device():
-        with torch.cuda.device(q_c.device), torch.cuda.stream(stream):
+    if stream is not None:
+        with _on(stream, q_c):
+            return tree_attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, w_uk, w_uv, max_nodes,
+                               masks, scales, scale, workspace)
+    if not q_c.is_cuda:
+        raise _b.MLAError(1, "tree_attend: q_c is on a CUDA device")
+    if q_c.device.index != torch.cuda.current_device():
+        with torch.cuda.device(q_c.device):
             return tree_attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, w_uk, w_uv, max_nodes,
                                masks, scales, scale, workspace)
     H, d_n, d_c = w_uk.shape

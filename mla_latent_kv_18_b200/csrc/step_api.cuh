@@ -61,6 +61,10 @@ mla_status append_slots(const mla_dims *dims, const void *ckv_new, int64_t ckv_n
     if (num_tokens < 0 || num_pages <= 0 || (layout != MLA_ROPE_INTERLEAVED && layout != MLA_ROPE_HALF))
         return MLA_ERR_INVALID_ARG;
     if (num_tokens == 0) return MLA_OK;
+    if (num_tokens == 1) {   // a stride that does not matter
+        ckv_new_stride = dims->d_latent;
+        kr_new_stride = dims->d_rope;
+    }
     if (!ckv_new || !kr_new || !slots || (positions && !inv_freq)) return MLA_ERR_INVALID_ARG;
     if (!aligned(ckv_new, 16) || (ckv_new_stride % 8) || ckv_new_stride < dims->d_latent ||
         kr_new_stride < dims->d_rope || !aligned(kr_new, 2) || !aligned(slots, 8) || !aligned(positions, 4) ||
@@ -101,6 +105,8 @@ mla_status append_slots(const mla_dims *dims, const void *ckv_new, int64_t ckv_n
                       0, static_cast<cudaStream_t>(stream), a);
 }
 
+constexpr int32_t kTreeMaxPages = (1 << 25) - 1;   // token indices, rounded up to a tile, fit 31 bits
+
 // Both cache formats of mla_decode_tree: ckv, or ckv8 and scales.
 mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, const mla_pool *ckv,
                        const mla_pool *ckv8, const float *scales, const mla_pool *kr, int32_t num_pages,
@@ -133,7 +139,8 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
     if ((st = check_pool(kr, one.d_rope)) != MLA_OK) return st;
     const int64_t rows = static_cast<int64_t>(num_tokens) * H;
     const double cost = (static_cast<double>(rows) / 64 + batch) * (static_cast<double>(max_pages) + 16);
-    if (rows >= (int64_t(1) << 31) || cost >= 2147483648.0 || num_parts > (1 << 20)) return MLA_ERR_UNSUPPORTED;
+    if (rows >= (int64_t(1) << 31) || cost >= 2147483648.0 || num_parts > (1 << 20) || max_pages >= kTreeMaxPages)
+        return MLA_ERR_UNSUPPORTED;
     if (workspace_bytes < mla_tree_workspace_bytes(&one, num_parts)) return MLA_ERR_INVALID_ARG;
     if ((st = step_ready()) != MLA_OK) return st;
 
@@ -336,13 +343,20 @@ mla_status mla_rotary(const mla_rotary_tensor *x, const mla_rotary_tensor *y, in
     int64_t heads = 0;
     bool copy = false;   // some tensor needs its other channels copied
     bool vec = width % E == 0 && offset % E == 0 && (layout == MLA_ROPE_HALF ? half : rot_dim) % E == 0;
+    mla_rotary_tensor kept[2];
     for (int i = 0; i < 2; ++i) {
-        const mla_rotary_tensor *t = both[i];
-        if (!t) continue;
+        if (!both[i]) continue;
+        // the stride of a dimension of one does not matter; an output whose rows fall together has none
+        mla_rotary_tensor *t = &kept[i];
+        *t = *both[i];
+        if (num_tokens == 1) t->in_token = t->out_token = 0;
+        else if (num_tokens > 1 && t->out_token == 0) return MLA_ERR_INVALID_ARG;
+        if (t->heads == 1) t->in_head = t->out_head = 0;
+        else if (t->heads > 1 && t->out_head == 0) return MLA_ERR_INVALID_ARG;
         if (t->heads < 0 || t->heads > 65536) return MLA_ERR_INVALID_ARG;
         if (num_tokens > 0 && t->heads > 0 && (!t->in || !t->out)) return MLA_ERR_INVALID_ARG;
         if (!aligned(t->in, size) || !aligned(t->out, size)) return MLA_ERR_INVALID_ARG;
-        if (t->in == t->out && (t->in_token != t->out_token || t->in_head != t->out_head)) return MLA_ERR_INVALID_ARG;
+        if (t->in && t->in == t->out && (t->in_token != t->out_token || t->in_head != t->out_head)) return MLA_ERR_INVALID_ARG;
         copy |= t->in != t->out;
         for (int64_t stride : {t->in_token, t->in_head, t->out_token, t->out_head}) vec &= stride % E == 0;
         vec &= aligned(t->in, 16) && aligned(t->out, 16);

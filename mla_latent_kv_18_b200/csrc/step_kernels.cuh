@@ -62,8 +62,8 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
     int32_t *cu = plan_smem, *fresh = plan_smem + a.batch + 1;   // exclusive sums, totals last
     __shared__ int64_t warp_sum[2][kPlanThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t cap = static_cast<int64_t>(a.max_pages) * 64;
     const int64_t big = 0x7FFFFFFF;
+    const int64_t cap = min(static_cast<int64_t>(a.max_pages) * 64, big);
     bool bad = false;
     // The kernel after this one reads the plan before its own dependency wait
     // (the decode calls' seq_lens and tables), so this one never lets it start early.
@@ -130,15 +130,16 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
     }
     if (total > a.num_tokens || head + pages > a.num_free) bad = true;
     auto fresh_page = [&](int64_t k) { return head + k < a.num_free ? a.free_pages[head + k] : -1; };
-    const int32_t first = blockIdx.x * kPlanThreads + tid, stride = gridDim.x * kPlanThreads;
+    // (indices are unsigned: a stride past the last of 2^31 - 1 does not wrap)
+    const uint32_t first = blockIdx.x * kPlanThreads + tid, stride = gridDim.x * kPlanThreads;
 
-    for (int32_t t = first; t < a.num_tokens; t += stride) {
+    for (uint32_t t = first; t < static_cast<uint32_t>(a.num_tokens); t += stride) {
         int32_t id = -1, pos = -1;
         int64_t slot = -1;
         uint32_t mask[kPlanMaxWords] = {};
-        if (t < total) {
+        if (t < static_cast<uint32_t>(total)) {
             id = plan_find(cu, a.batch, t);
-            const int32_t i = t - cu[id];
+            const int32_t i = static_cast<int32_t>(t) - cu[id];
             const int64_t c = a.cached_lens[id], at = c + i;
             const int64_t pg = at / 64 - (c + 63) / 64;
             const int32_t page = pg < 0 ? a.block_table[static_cast<int64_t>(id) * a.max_pages + at / 64]
@@ -173,12 +174,12 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
                 if (w < a.words) a.masks[static_cast<int64_t>(t) * a.words + w] = mask[w];
         }
     }
-    for (int32_t k = first; k < pages; k += stride) {
-        const int32_t b = plan_find(fresh, a.batch, k);
+    for (uint32_t u = first; u < static_cast<uint32_t>(pages); u += stride) {
+        const int32_t k = static_cast<int32_t>(u), b = plan_find(fresh, a.batch, k);
         const int64_t p0 = (static_cast<int64_t>(a.cached_lens[b]) + 63) / 64;
         a.block_table[static_cast<int64_t>(b) * a.max_pages + p0 + (k - fresh[b])] = fresh_page(k);
     }
-    for (int32_t b = first; b <= a.batch; b += stride) {
+    for (int32_t b = static_cast<int32_t>(first); b <= a.batch; b += static_cast<int32_t>(stride)) {
         a.cu_tokens[b] = cu[b];
         if (b < a.batch) {
             int64_t c, n;

@@ -76,7 +76,10 @@ int device_of(PyObject *o, const char *call, const char *name) {
 
 int64_t integer(PyObject *o, const char *call, const char *name, int64_t lo, int64_t hi) {
     int over = 0;
-    const int64_t v = PyLong_Check(o) ? PyLong_AsLongLongAndOverflow(o, &over) : (over = 1, 0);
+    PyObject *whole = PyNumber_Index(o);   // Python's and numpy's integers
+    const int64_t v = whole ? PyLong_AsLongLongAndOverflow(whole, &over) : (over = 1, 0);
+    Py_XDECREF(whole);
+    PyErr_Clear();
     if (over || v < lo || v > hi)
         throw Refused{MLA_ERR_INVALID_ARG, std::string(call) + ": " + name + " is a whole number in range"};
     return v;
@@ -255,6 +258,7 @@ PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t) {
         }
         const int64_t offset = integer(a[5], call, "offset", 0, 65536);
         const int inverse = PyObject_IsTrue(a[6]);
+        if (inverse < 0) throw python_error();
         check(mla_rotary(&arg[0], n == 2 ? &arg[1] : nullptr, dtype, static_cast<int32_t>(x.size(0)),
                          static_cast<int32_t>(x.size(2)), static_cast<int32_t>(offset),
                          static_cast<int32_t>(2 * freq.numel()), ptr<int32_t>(pos), ptr<double>(freq),

@@ -137,12 +137,22 @@ __device__ inline TreePlan tree_find(const TreeBatch &t, int32_t part, int32_t n
     const int32_t W = t.gap;
     bool bad = false;
     int32_t N = 0, items = 0;
+    uint32_t tokens = 0;
     TreeSeq first = {};   // this lane's sequence of the first 32, kept for the second pass
     for (int32_t base = 0; base < t.batch; base += 32) {
         const int32_t b = base + lane;
         TreeSeq q = {};
         if (b < t.batch) q = tree_seq(t, b, tile_tokens, item_rows, &bad);
         if (base == 0) first = q;
+        // Where cu_tokens turns back, sequences can overlap and hold more tokens together than
+        // there are; the costs would pass the 32 bits that the host has checked. Such a step is
+        // not run.
+        tokens += __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(q.nodes));
+        if (tokens > static_cast<uint32_t>(t.total_tokens)) {
+            bad = true;
+            items = 0;
+            break;
+        }
         N += __reduce_add_sync(0xffffffffu, q.blocks * q.tiles);
         items += __reduce_add_sync(0xffffffffu, q.blocks);
     }

@@ -57,6 +57,11 @@ def test_tree_refusals(b, kw, status):
     assert _tree(b, **kw) == status
 
 
+def test_tree_refuses_tables_past_31_bits(b):
+    assert _tree(b, T=1, B=1, max_pages=(1 << 25) - 1) == UNSUPPORTED
+    assert _tree(b, T=1, B=1, max_pages=1 << 27) == UNSUPPORTED
+
+
 def test_tree_refuses_bad_pools_and_dims(b):
     assert _tree(b, ckv=b.MLAPool(P + 2, 64 * 512, 512)) == INVALID
     assert _tree(b, ckv=b.MLAPool(P, 64 * 512, 256)) == INVALID
@@ -117,6 +122,13 @@ def _rot(b, x=None, y=None, dtype=0, T=4, width=64, offset=0, rot=64, pos=P, fre
     dict(rot=4098, width=5000), dict(freq=P + 4)])
 def test_rotary_refusals(b, kw):
     assert _rot(b, **kw) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(out_token=0), dict(out_head=0), dict(src=2 * P, out_token=0)])
+def test_rotary_refuses_outputs_that_fall_together(b, kw):
+    assert _rot(b, **kw) == INVALID
+    y = b.MLARotaryTensor(src=P, out=2 * P, in_token=0, in_head=0, out_token=64, out_head=0, heads=2)
+    assert _rot(b, y=y) == INVALID
 
 
 def test_rotary_refuses_rows_too_wide(b):
@@ -221,6 +233,31 @@ def test_python_entry_points_refuse_cpu_tensors_and_wrong_shapes(api, b):
         api.append_kv_slots(ckv[0], kr[0], torch.zeros(64, dtype=torch.int64), ckv, kr, dims)
     with pytest.raises(b.MLAError):
         api.append_kv_slots(ckv[0], kr[0], i32(64), ckv, kr, dims)
+
+
+def test_streams_of_another_device_are_refused(api, b):
+    """`stream` has to be one of the tensors' device (the check comes before anything else)."""
+    class Stream:
+        device = torch.device("cuda", 1)
+    s, x = Stream(), torch.zeros(2, 4, 64)
+    i32 = torch.zeros(2, 4, dtype=torch.int32)
+    for call in (lambda: api.rotary(x, i32, x, stream=s),
+                 lambda: api.step_plan(i32, i32, i32, i32, i32, 8, stream=s),
+                 lambda: api.append_kv_slots(x, x, i32, x, x, None, stream=s),
+                 lambda: api.append_kv_slots_fp8(x, x, i32, x, x, x, None, stream=s),
+                 lambda: api.decode_tree(x, x, x, i32, i32, i32, None, 8, stream=s),
+                 lambda: api.decode_tree_fp8(x, x, x, x, i32, i32, i32, None, 8, stream=s),
+                 lambda: api.tree_attend(x, x, x, x, i32, i32, i32, x, x, 8, stream=s)):
+        with pytest.raises(b.MLAError, match="stream of cuda:1, tensors on cpu"):
+            call()
+
+
+def test_tree_attend_refuses_cpu_tensors(api, b):
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(b.MLAError):
+        api.tree_attend(z(8, 16, 128), z(8, 16, 64), z(4, 64, 512), z(4, 64, 64), i32(2, 4), i32(2), i32(3),
+                        z(16, 128, 512), z(16, 512, 128), 8)
 
 
 def test_rotary_tensor_struct_matches_the_header(b):

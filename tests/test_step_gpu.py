@@ -285,6 +285,38 @@ def test_append_slots_bad_slots_are_skipped(api):
     assert api.get_device_error() == 4 and (kr.view(128, 64)[:6] == 1).all()
 
 
+def test_single_rows_empty_calls_and_whole_numbers(api):
+    """One token, whose strides say nothing; no token; sizes as numpy's integers."""
+    import numpy as np
+    dims = api.make_dims(1, 1, 128, 512, 64, 128)
+    f, m = api.rope_frequencies(64, device="cuda")
+    g = torch.Generator("cuda").manual_seed(2)
+    c, k = (torch.randn(n, 1, generator=g, device="cuda").bfloat16().as_strided((1, n), (1, 1)) for n in (512, 64))
+    pool, kr = torch.zeros(2, 64, 512, device="cuda").bfloat16(), torch.zeros(2, 64, 64, device="cuda").bfloat16()
+    api.append_kv_slots(c, k, torch.tensor([70], device="cuda"), pool, kr, dims, _i32([3]), f, m)
+    assert torch.equal(pool[1, 6], c[0]) and (pool[0] == 0).all()
+    _turn_check(kr[1, 6][None, None], k[:, None], _i32([3]), f, m, "interleaved", 0)
+    x = k.as_strided((1, 1, 64), (1, 3, 1))
+    _turn_check(api.rotary(x, _i32([3]), f, m), x, _i32([3]), f, m, "interleaved", 0)
+    # broadcast inputs: every token's row is the same one
+    x = torch.randn(1, 2, 64, generator=g, device="cuda").bfloat16().expand(5, 2, 64)
+    _turn_check(api.rotary(x, _i32([0, 1, 2, 3, 4]), f, m), x, _i32([0, 1, 2, 3, 4]), f, m, "interleaved", 0)
+    # nothing to do
+    before = pool.clone()
+    api.append_kv_slots(c[:0], k[:0], torch.zeros(0, dtype=torch.int64, device="cuda"), pool, kr, dims, _i32([]), f, m)
+    assert api.rotary(x[:0], _i32([]), f, m).shape == (0, 2, 64)
+    assert api.rotary(x[:, :0], _i32([0] * 5), f, m).shape == (5, 0, 64)
+    assert torch.equal(pool, before)
+    table = _i32([[4, -1]])
+    p = api.step_plan(_i32([60]), _i32([6]), _i32([9]), _i32([0]), table, np.int64(6), _i32(list(range(-1, 5))),
+                      np.int32(8))
+    assert p.slots.tolist() == [4 * 64 + 60 + i for i in range(4)] + [9 * 64, 9 * 64 + 1] and table.tolist() == [[4, 9]]
+    with pytest.raises(Exception, match="whole number"):
+        api.step_plan(_i32([60]), _i32([6]), _i32([9]), _i32([0]), table, 6.0)
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 0
+
+
 # ------------------------------------------------------------------ a step, as it is used
 
 @pytest.mark.parametrize("fp8", [False, True])

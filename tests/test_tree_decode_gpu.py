@@ -320,6 +320,34 @@ def test_tree_bad_data_is_reported_and_skipped(api):
             check_tree(o[at], lse[at], ref, s.lens[b])
 
 
+@pytest.mark.parametrize("dc", [512, 64])
+def test_tree_with_offsets_that_turn_back_is_not_run(api, dc):
+    """Sequences that overlap, with more tokens together than q holds: the device error, nothing written."""
+    s = Step(api, heads=16, counts=[40] + [0] * 79, lens=[64] * 80, dc=dc)
+    s.cu = torch.tensor([40 * (b & 1) for b in range(81)], dtype=torch.int32, device="cuda")   # 40 x [0, 40)
+    o = torch.full((s.T, 16, dc), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((s.T, 16), 7.0, device="cuda")
+    s.run(o_lat=o, lse_out=lse)
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 4
+    assert (o == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("dc", [512, 64])
+def test_tree_without_tokens_or_sequences(api, dc):
+    s = Step(api, heads=16, counts=[3], lens=[70], dc=dc)
+    masks, kw = s.masks(), dict(max_nodes=s.max_nodes, dims=s.dims)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    o, lse = api.decode_tree(s.q[:0], s.ckv, s.kr, s.block_table, s.seq_lens, torch.zeros(2, **i32), masks=masks[:0], **kw)
+    assert o.shape == (0, 16, dc) and lse.shape == (0, 16)
+    o = torch.full((s.T, 16, dc), 7.0, dtype=torch.bfloat16, device="cuda")
+    api.decode_tree(s.q, s.ckv, s.kr, s.block_table[:0], s.seq_lens[:0], torch.zeros(1, **i32), masks=masks, o_lat=o, **kw)
+    api.decode_tree(s.q, s.ckv, s.kr, s.block_table, s.seq_lens, torch.zeros(2, **i32), masks=masks, o_lat=o, **kw)
+    assert (o == 7).all()
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 0
+
+
 def test_tree_captured_replayed_and_on_two_streams(api):
     """A captured step replayed on new lengths; two streams at once, each with its workspace."""
     a = Step(api, heads=64, counts=[6, 1, 9], lens=[900, 10, 300], seed=1)
