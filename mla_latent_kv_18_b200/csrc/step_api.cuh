@@ -383,6 +383,7 @@ mla_status mla_rotary(const mla_rotary_tensor *x, const mla_rotary_tensor *y, in
     const int32_t e = vec ? E : 1;
     a.turned = !vec ? half : layout == MLA_ROPE_HALF ? half / e : rot_dim / e;
     a.copied = copy ? (width - rot_dim) / e : 0;
+    if (layout == MLA_ROPE_HALF) a.copied = (a.copied + 1) / 2;   // two vectors a place
     const int64_t places = heads * (static_cast<int64_t>(a.turned) + a.copied);
     const int64_t across = (places + mla::kRotaryThreads - 1) / mla::kRotaryThreads;   // <= 65536
     if (across > 65535) return MLA_ERR_UNSUPPORTED;

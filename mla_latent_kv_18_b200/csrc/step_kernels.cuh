@@ -293,11 +293,14 @@ __global__ void __launch_bounds__(kRotaryThreads, kVec && !kHalf ? 5 : 3) rotary
     const int32_t place = n - h * per_head;
     const bool active = h < a.heads[0] + a.heads[1];
     if (!active) h = 0;
-    // copied channels before the turned ones, those, and the copied ones after
-    const int32_t before = a.copied ? a.offset / E : 0;
+    // kHalf: the turned places, then the copied vectors, two a place as well; else copied
+    // channels before the turned ones, those, and the copied ones after
+    const int32_t before = a.copied && !kHalf ? a.offset / E : 0;
     const bool turns = place >= before && place < before + a.turned;
     const int32_t item = place - before;
+    auto copied = [&](int32_t j) { return j * E < a.offset ? j * E : j * E + 2 * a.half; };   // channel of the j-th
     const int32_t c = turns            ? a.offset + item * (kHalf || kVec ? E : 2)
+                      : kHalf          ? copied(item - a.turned)
                       : place < before ? place * E
                                        : a.offset + 2 * a.half + (item - a.turned) * E;
     const int w = h >= a.heads[0] ? 1 : 0;
@@ -306,8 +309,10 @@ __global__ void __launch_bounds__(kRotaryThreads, kVec && !kHalf ? 5 : 3) rotary
     const T *in = static_cast<const T *>(x.in) + static_cast<int64_t>(t0) * x.in_token + h * x.in_head + c;
     T *out = static_cast<T *>(x.out) + static_cast<int64_t>(t0) * x.out_token + h * x.out_head + c;
     const int64_t in_token = x.in_token, out_token = x.out_token;
-    const bool two = turns && (kHalf || !kVec);      // the pair's other half is apart
-    const int32_t apart = kHalf ? a.half : 1;
+    // a second vector: the pair's other half, or another copied one
+    const int32_t next = item - a.turned + a.copied;
+    const bool two = turns ? kHalf || !kVec : kHalf && next * E < a.width - 2 * a.half;
+    const int32_t apart = !kHalf ? 1 : turns ? a.half : copied(next) - c;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     Vec lo[U], hi[U];
