@@ -237,8 +237,8 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
 }
 
 template <typename T>
-mla_status launch_rotary(const mla::RotaryArgs &a, bool half, bool vec, dim3 grid, uint32_t smem, cudaStream_t s) {
-    const dim3 block(mla::kRotaryThreads);
+mla_status launch_rotary(const mla::RotaryArgs &a, bool half, bool vec, dim3 grid, dim3 block, uint32_t smem,
+                         cudaStream_t s) {
     if (half)
         return vec ? launch_pdl(mla::rotary_kernel<T, true, true>, grid, block, smem, s, a)
                    : launch_pdl(mla::rotary_kernel<T, true, false>, grid, block, smem, s, a);
@@ -387,6 +387,7 @@ mla_status mla_rotary(const mla_rotary_tensor *x, const mla_rotary_tensor *y, in
     const int64_t places = heads * (static_cast<int64_t>(a.turned) + a.copied);
     const int64_t across = (places + mla::kRotaryThreads - 1) / mla::kRotaryThreads;   // <= 65536
     if (across > 65535) return MLA_ERR_UNSUPPORTED;
+    const dim3 block(static_cast<unsigned>(((places + across - 1) / across + 31) / 32 * 32));   // even shares
     // Tokens of a CTA: 16, while their table fits and eight CTAs per SM are left.
     int64_t tt = std::min<int64_t>(16, mla::kRotaryMaxTable / half);
     while (tt > 1 && (num_tokens + tt - 1) / tt * across < 8 * static_cast<int64_t>(device_sms())) tt /= 2;
@@ -395,9 +396,9 @@ mla_status mla_rotary(const mla_rotary_tensor *x, const mla_rotary_tensor *y, in
     const uint32_t smem = static_cast<uint32_t>(tt * half * sizeof(float2));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool h = layout == MLA_ROPE_HALF;
-    if (dtype == MLA_BF16) return launch_rotary<__nv_bfloat16>(a, h, vec, grid, smem, s);
-    if (dtype == MLA_FP16) return launch_rotary<__half>(a, h, vec, grid, smem, s);
-    return launch_rotary<float>(a, h, vec, grid, smem, s);
+    if (dtype == MLA_BF16) return launch_rotary<__nv_bfloat16>(a, h, vec, grid, block, smem, s);
+    if (dtype == MLA_FP16) return launch_rotary<__half>(a, h, vec, grid, block, smem, s);
+    return launch_rotary<float>(a, h, vec, grid, block, smem, s);
 }
 
 mla_status mla_append_kv_slots(const mla_dims *dims, const void *ckv_new, int64_t ckv_new_stride, const void *kr_new,

@@ -247,12 +247,14 @@ struct Elem<float> {
 // heads of its own, in one launch: channels offset .. offset + rot of every head are
 // turned pair by pair, the others copied where the output is another tensor.
 // A thread has one place of a token's rows (a head's vector of 16 bytes; in the half
-// layout one of each half; where strides or widths do not allow that (kVec), a pair or a
-// channel) and walks TT tokens with it, the loads of four of them in flight, so no index is
-// divided in the loop; a CTA's 256 places share the TT * rot / 2 cosines and sines, made while
-// the first loads are on their way.
+// layout one of each half, or two copied ones (290 us below with one); where strides or widths
+// do not allow that (kVec), a pair or a channel) and walks TT tokens with it, the loads of four
+// of them in flight, so no index is divided in the loop; a CTA's up to 256 places share the
+// TT * rot / 2 cosines and sines, made while the first loads are on their way. The CTAs of
+// a row have equal shares of its places, not 256 and a rest (4096 tokens x 4 heads of 128 fp32:
+// 3.8 us, not 8.1).
 // Bound by HBM for prompts (every byte once in and once out), by latency for a
-// step's tokens. 16384 tokens x 129 heads of 192, 64 of them turned: 288 us, 5.6 TB/s (253 us interleaved).
+// step's tokens. 16384 tokens x 129 heads of 192, 64 of them turned: 259 us, 6.3 TB/s (255 us interleaved).
 // ---------------------------------------------------------------------------
 struct RotaryTensor {
     const void *in;
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(kRotaryThreads, kVec && !kHalf ? 5 : 3) rotary
     };
     const int32_t t0 = blockIdx.x * a.TT, nt = min(a.TT, a.tokens - t0);
     // this thread's place: head h of both tensors' and channel c
-    const int32_t n = blockIdx.y * kRotaryThreads + threadIdx.x, per_head = a.turned + a.copied;
+    const int32_t n = blockIdx.y * blockDim.x + threadIdx.x, per_head = a.turned + a.copied;
     int32_t h = n / per_head;
     const int32_t place = n - h * per_head;
     const bool active = h < a.heads[0] + a.heads[1];
@@ -331,8 +333,8 @@ __global__ void __launch_bounds__(kRotaryThreads, kVec && !kHalf ? 5 : 3) rotary
         }
     };
     fetch(0);
-    for (int i = threadIdx.x; i < nt; i += kRotaryThreads) s_pos[i] = a.positions[t0 + i];
-    for (int i = threadIdx.x; i < nt * a.half; i += kRotaryThreads) {
+    for (int i = threadIdx.x; i < nt; i += blockDim.x) s_pos[i] = a.positions[t0 + i];
+    for (int i = threadIdx.x; i < nt * a.half; i += blockDim.x) {
         const int t = i / a.half, p = i - t * a.half;
         const float2 cs = rotary_cos_sin(a.positions[t0 + t], a.inv_freq[p], a.mscale);
         rotary_cs[i] = make_float2(cs.x, a.sign * cs.y);
