@@ -402,11 +402,6 @@ __device__ __forceinline__ void dequant_slot(uint32_t slot, uint32_t blk, int wr
     }
 }
 
-// E4M3 pair kernel: one dequantising warp's share of one slot: wait until the
-// slot's codes and scales have landed, widen them, report the slot full on the
-// leader's barrier. The scales (32 consecutive tokens, from slot row sc_row0
-// on) arrive by TMA in the warp's own last row of block NBOX - 1, which the
-// warp itself overwrites in its first step, after reading them.
 // Where a segment's query rows are: rows q_row0 .. + seg_rows of plane q_seq of q
 // (kTree: q is one plane of packed rows).
 __device__ __forceinline__ int32_t q_row0(const SegmentWalker &) { return 0; }
@@ -420,6 +415,11 @@ __device__ __forceinline__ int64_t first_row(const SegmentWalker &w, const Decod
 }
 __device__ __forceinline__ int64_t first_row(const TreeWalker &w, const DecodeArgs &) { return w.row0; }
 
+// E4M3 pair kernel: one dequantising warp's share of one slot: wait until the
+// slot's codes and scales have landed, widen them, report the slot full on the
+// leader's barrier. The scales (32 consecutive tokens, from slot row sc_row0
+// on) arrive by TMA in the warp's own last row of block NBOX - 1, which the
+// warp itself overwrites in its first step, after reading them.
 template <int NBOX, int NPAIR, class Walker>
 __device__ __forceinline__ bool dequant_tile(const TileCursor<Walker> &cur, int64_t k, const DecodeArgs &args,
                                              uint32_t ring, uint32_t stage, uint32_t blk, int nst,
