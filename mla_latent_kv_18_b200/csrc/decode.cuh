@@ -120,7 +120,7 @@ __device__ __forceinline__ uint4 finite_or_zero(uint4 v) {
 constexpr int kDecodeThreads = 192;          // single kernel: 6 warps
 constexpr int kPairThreads = 352;            // pair kernel: 11 warps (6 = P.V-slot producer, 7..10 segment warps)
 constexpr int kSegWarp0 = 7;                 // pair kernel: first of the four segment warps
-constexpr int kPairThreadsFp8 = 480;         // E4M3 pair kernel: + 4 dequantising warps (11..14)
+constexpr int kPairThreadsFp8 = 608;         // E4M3 pair kernel: + 8 dequantising warps (11..14 QK^T, 15..18 P.V)
 constexpr int kDqWarp0 = 11;
 constexpr int kSoftmaxWarp0 = 2;             // warps 2..5
 constexpr float kRescaleThreshold = 8.0f;    // log2 units: rescale O when max grows > 2^8
@@ -261,7 +261,7 @@ constexpr int TREE_WHOLE = 10;
 // kTree: cost of a switch in tiles, measured: 16 ragged sequences of up to 4096 tokens,
 // 4 nodes, bf16 cache 42.0 us with 8, 39.8 with 6, 44.8 with 14 (16 equal ones with 8 nodes:
 // 155.0, 155.4, 154.7); E4M3 cache, whose tiles take longer, 65.1 us with 8, 59.9 with 5,
-// 70.2 with 14.
+// 70.2 with 14 (before its rings were widened by warps of their own: 57.3 now).
 constexpr int TREE_GAP = 6, TREE_GAP_FP8 = 5;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TMEM_O = 0;                 // two 128-column accumulators (c = 0, 1)
@@ -641,8 +641,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
             if (!kFp8 && qk && walk.primed) {
                 // the first segment's Q: blocks 0..QT-1 to the staging area (the
                 // segment warps move them to tensor memory), the rest to their place.
-                // (The E4M3 kernel loads it like any other segment's: at its
-                // 128-register cap the staged path made the dequantising warps spill.)
+                // (The E4M3 kernel loads it like any other segment's: at a 128-register
+                // cap the staged path made the dequantising warps spill, and 19 warps have 96.)
                 const uint32_t qbar = bar(&misc->q_tma);
                 ptx::mbar_arrive_expect_tx(qbar, NB * ROWS_CTA * 128);
                 for (int j = 0; j < NB; ++j)
@@ -850,32 +850,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
     } else if (kFp8 && warp >= kDqWarp0) {
         // ------------------------------------------------------ dequantising warps
         if constexpr (kFp8) {
-            const int dq = warp - kDqWarp0;
-            // every warp takes 8 of a QK^T slot's 32 rows and 16 of a P.V slot's
-            // 64, converting QK^T one tile ahead of P.V (the MMAs consume them in
-            // that order); the scale copies hold the CTA's 32 QK^T tokens and
-            // P.V tokens 32 (dq / 2) + [0, 32)
-            TileCursor<Walker> cq, cp;
-            cq.w = walk;
-            cq.start();
-            cp = cq;
-            int64_t kq = 0, kp = 0;
+            // Four warps take 8 of a QK^T slot's 32 rows each, four 16 of a P.V slot's 64: neither
+            // ring's conversion waits for the other's codes or for its fence (16 sequences of
+            // 65536 tokens: 471 us a step, 503 with four warps that did both in turn). The scale
+            // copies hold the CTA's 32 QK^T tokens and P.V tokens 32 (dq / 2) + [0, 32).
+            const int dq = (warp - kDqWarp0) & 3;
+            const bool qk = warp - kDqWarp0 < 4;
+            TileCursor<Walker> cur;
+            cur.w = walk;
+            cur.start();
             bool ok = true;
-            auto qk_tile = [&]() {
-                ok = dequant_tile<4, 1>(cq, kq, args, base + OFF_QK, STAGE_QK, OWN * 128, QK_STAGES, misc->code_qk,
-                                        misc->qk_full, 8 * dq, 0, OWN * static_cast<int>(rank), rank, lane,
-                                        abort_flag);
-                cq.advance();
-                ++kq;
-            };
-            if (cq.have) qk_tile();
-            while (ok && cp.have && !*abort_flag) {
-                if (cq.have) qk_tile();
-                if (!ok) break;
-                ok = dequant_tile<2, 2>(cp, kp, args, base + OFF_PV, STAGE_PV, TOK * 128, PV_STAGES, misc->code_pv,
-                                        misc->pv_full, 16 * dq, 32 * (dq >> 1), 0, rank, lane, abort_flag);
-                cp.advance();
-                ++kp;
+            for (int64_t k = 0; ok && cur.have && !*abort_flag; ++k) {
+                ok = qk ? dequant_tile<4, 1>(cur, k, args, base + OFF_QK, STAGE_QK, OWN * 128, QK_STAGES, misc->code_qk,
+                                             misc->qk_full, 8 * dq, 0, OWN * static_cast<int>(rank), rank, lane,
+                                             abort_flag)
+                        : dequant_tile<2, 2>(cur, k, args, base + OFF_PV, STAGE_PV, TOK * 128, PV_STAGES, misc->code_pv,
+                                             misc->pv_full, 16 * dq, 32 * (dq >> 1), 0, rank, lane, abort_flag);
+                cur.advance();
             }
         }
     } else if (warp >= kSegWarp0) {
@@ -906,24 +897,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
         // The loads are issued in three rounds of independent requests (half of
         // the shared-memory blocks with each of the first two), so a segment
         // start costs three global-load latencies rather than one per block.
+        // (E4M3: five rounds of one block, for its 96 registers.)
         auto load_q = [&](const Walker &w) {
             const __nv_bfloat16 *qb = args.q + first_row(w, args) * D;
             const int32_t rows = seg_rows(w, args);
             const bool real_row = grow < rows;
             const __nv_bfloat16 *qrow = qb + static_cast<int64_t>(real_row ? grow : 0) * D;
-            constexpr int NSM = ROWS_CTA * (NB - QT) * 8 / 128 / 2;   // 8 + 8 chunks of blocks 5..8
+            constexpr int BL = kFp8 ? 1 : 2;                               // 64-channel blocks per round, at most
+            constexpr int NSM = ROWS_CTA * (NB - QT) * 8 / 128 * BL / 4;   // of 16 chunks of blocks 5..8
 #pragma unroll 1
-            for (int j0 = 0; j0 < QT; j0 += 2) {   // up to two 64-channel blocks per round
-                const int nj = (j0 + 1 < QT) ? 2 : 1;
-                uint4 v[16], sv[NSM];
+            for (int j0 = 0; j0 < QT; j0 += BL) {
+                const int nj = (j0 + BL <= QT) ? BL : 1;
+                uint4 v[8 * BL], sv[NSM];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 8 * BL; ++i)
                     v[i] = (real_row && (i < 8 || nj == 2)) ? ld_global_nc_v4(qrow + 64 * j0 + 8 * i)
                                                             : make_uint4(0, 0, 0, 0);
                 if (j0 < 4) {
 #pragma unroll
                     for (int i = 0; i < NSM; ++i) {
-                        const int idx = st_tid + 128 * (i + NSM * (j0 >> 1));
+                        const int idx = st_tid + 128 * (i + NSM * (j0 / BL));
                         const int r = idx / ((NB - QT) * 8);
                         const int cc = idx - r * ((NB - QT) * 8);   // 16-byte chunk among blocks 5..8
                         const int gr = ROWS_CTA * static_cast<int>(rank) + r;
@@ -933,7 +926,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                     }
 #pragma unroll
                     for (int i = 0; i < NSM; ++i) {
-                        const int idx = st_tid + 128 * (i + NSM * (j0 >> 1));
+                        const int idx = st_tid + 128 * (i + NSM * (j0 / BL));
                         const int r = idx / ((NB - QT) * 8);
                         const int cc = idx - r * ((NB - QT) * 8);
                         st_shared_v4(base + OFF_Q + (cc >> 3) * (ROWS_CTA * 128) + sw128(r, cc & 7), sv[i].x,
@@ -941,7 +934,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                     }
                 }
 #pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
+                for (int jj = 0; jj < BL; ++jj) {
                     if (jj >= nj) break;
                     uint32_t w[32];
 #pragma unroll
