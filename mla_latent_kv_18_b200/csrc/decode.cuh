@@ -414,6 +414,9 @@ __device__ __forceinline__ int64_t first_row(const SegmentWalker &w, const Decod
     return static_cast<int64_t>(w.seg_b) * a.rows;
 }
 __device__ __forceinline__ int64_t first_row(const TreeWalker &w, const DecodeArgs &) { return w.row0; }
+// The tile that a segment's position t stands for.
+__device__ __forceinline__ int64_t tile_at(const SegmentWalker &, int64_t t) { return t; }
+__device__ __forceinline__ int64_t tile_at(const TreeWalker &w, int64_t t) { return w.tile_at(static_cast<int32_t>(t)); }
 
 // E4M3 pair kernel: one dequantising warp's share of one slot: wait until the
 // slot's codes and scales have landed, widen them, report the slot full on the
@@ -439,7 +442,7 @@ __device__ __forceinline__ bool dequant_tile(const TileCursor<Walker> &cur, int6
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sc[i]) : "r"(slot + sc_off + 4 * (r - sc_row0)) : "memory");
     }
     __syncwarp();   // the scale row is overwritten below
-    const int32_t rlim = cur.w.L - static_cast<int32_t>(cur.t) * pair::TOK - tok_off;
+    const int32_t rlim = cur.w.L - static_cast<int32_t>(tile_at(cur.w, cur.t)) * pair::TOK - tok_off;
     dequant_slot<NBOX, NPAIR>(slot, blk, wrow0, lane, rlim, sc);
     ptx::fence_proxy_async_smem();
     __syncwarp();
@@ -533,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                     const int32_t *trow0 = args.block_table + static_cast<int64_t>(w0.seg_b) * args.max_pages;
 #pragma unroll
                     for (int i = 0; i < FIRST_PAGES; ++i)
-                        pg[i] = (w0.t_begin + i < w0.t_end) ? trow0[w0.t_begin + i] : 0;
+                        pg[i] = (w0.t_begin + i < w0.t_end) ? trow0[w0.tile_at(w0.t_begin + i)] : 0;
                 }
                 ptx::prefetch_tensormap(&map_ckv32);
                 ptx::prefetch_tensormap(&map_ckv64);
@@ -663,7 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                     // first segment's tiles first)
                     int32_t page = (first_seg && k < FIRST_PAGES)
                                        ? reinterpret_cast<const int32_t *>(smem + OFF_FIRST_PAGES)[k]
-                                       : trow[t];
+                                       : trow[tile_at(walk, t)];
                     if (page < 0 || page >= args.num_pages) { bad_page = true; page = 0; }
                     if (use >= 1 && !wait_bounded(bar(&emptyb[s]), (use - 1) & 1, abort_flag,
                                                   args.timeout_ns))
@@ -1146,7 +1149,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
             for (int64_t t = t_begin; t < t_end; ++t, ++k) {
                 const int s = static_cast<int>(k & 1);          // P buffer, exchange words
                 const int sb = static_cast<int>(k % NSB);       // score buffer
-                const int32_t tok0 = static_cast<int32_t>(t) * TOK + half * OWN;
+                const int32_t tile = static_cast<int32_t>(tile_at(walk, t));
+                const int32_t tok0 = tile * TOK + half * OWN;
                 uint32_t bits = 0;   // kTree: which of the 32 tokens this row sees, read before the scores land
                 if (kTree && real_row)
                     bits = tok0 + 32 <= vis ? ~0u : tree_bits(mask, args.mask_words, node, nodes, tok0 - vis);
@@ -1249,7 +1253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                 // with the page and may hold any bits (an unwritten or recycled page
                 // slot). Their P is 0, but 0 * NaN = NaN in the value product, so
                 // they are cleared in this CTA's P.V slot once it has landed.
-                const int32_t valid = L - static_cast<int32_t>(t) * TOK;
+                const int32_t valid = L - tile * TOK;
                 if (!kFp8 && valid < TOK) {   // (E4M3: the dequantising warps wrote zeros there)
                     const int ps = static_cast<int>(k % PV_STAGES);
                     if (!wait_bounded(bar(&misc->pv_landed[ps]), (k / PV_STAGES) & 1, abort_flag,

@@ -67,7 +67,7 @@ struct TreeShared {
 struct TreeWalker {
     TreeBatch batch;
     int32_t tile_tokens, item_rows, part;
-    int32_t tile, te;             // cost position reached, end of this partition's range
+    int32_t ts, tile, te;         // this partition's range on the cost axis: start, position reached, end
     int32_t C, P;                 // total cost, partitions in use
     int32_t b, blk, O;            // the next item: sequence, row block, cost offset
     bool later;                   // a segment has been handed out
@@ -75,6 +75,14 @@ struct TreeWalker {
     // current segment
     int32_t seg_b, L, nodes, first_tok, row0, rows, t_begin, t_end, slot;   // slot < 0: the whole item
     int32_t item_end;             // cost position after the item's last tile
+    int32_t rot;                  // tiles skipped at first and taken last: see tile_at
+
+    // The t-th position of the segment (t_begin <= t < t_end) as a tile. Partitions advance a tile
+    // at a time together, so position x of a partition is a clock that all of them share: a
+    // segment starts at tile x mod (tiles of its sequence), if it has that tile, and wraps around.
+    // Row blocks of one sequence, in different partitions or one after another, then read the
+    // same tile at the same time, one of them from HBM and the others from L2.
+    __device__ int32_t tile_at(int32_t t) const { return t + rot < t_end ? t + rot : t + rot - (t_end - t_begin); }
 
     // The current segment's note, if its item begins here and goes on.
     __device__ TreeShared shared() const {
@@ -113,6 +121,8 @@ struct TreeWalker {
             slot = (t_begin == 0 && t_end == q.tiles) ? -1 : 2 * part + (later ? 1 : 0);
             later = true;
             tile = at + t_end;
+            const int32_t s = (at + t_begin - ts) % q.tiles;
+            rot = s > t_begin && s < t_end ? s - t_begin : 0;
             return true;
         }
         return false;
@@ -210,7 +220,7 @@ __device__ inline TreeWalker tree_start(const TreeBatch &t, int32_t part, int32_
     w.C = p.C;
     w.P = p.P;
     if (part < p.P) {
-        w.tile = static_cast<int32_t>(part_start(part, p.C, p.P));
+        w.ts = w.tile = static_cast<int32_t>(part_start(part, p.C, p.P));
         w.te = static_cast<int32_t>(part_start(part + 1, p.C, p.P));
     }
     w.b = p.b;
