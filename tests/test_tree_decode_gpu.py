@@ -143,6 +143,18 @@ def test_tree_partition_counts(api, parts, dc):
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("parts", [2, 3, 5, 11, 74])
+def test_tree_blocks_that_start_inside_a_sequence(api, fp8, parts):
+    """Several row blocks of long sequences: partitions whose segments start at any tile and wrap around,
+    over the drafted tokens and the end of the sequence too."""
+    s = Step(api, heads=128, counts=[9, 2, 12], lens=[3001, 777, 2100], seed=parts, fp8=fp8)
+    o, lse = s.run(num_parts=parts)
+    s.check(o, lse)
+    again = s.run(num_parts=parts)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
 @pytest.mark.parametrize("dc", [512, 64])
 def test_tree_chain_is_the_chain_mask(api, dc):
     s = Step(api, heads=24, counts=[6, 1, 40], lens=[500, 64, 41], dc=dc, kind="chain")
