@@ -60,8 +60,11 @@ struct DecodeArgs {
     int32_t rows;                // R = n_q * heads (<= 128)
     float scale;                 // softmax scale
     float scale_log2;            // scale * log2(e)
-    // kTree only: q, o_lat and lse_out are packed by token, the workspace holds
-    // 2 num_parts slots of item_rows rows
+};
+
+// A step of packed query tokens: q, o_lat and lse_out are packed by token, the workspace
+// holds 2 num_parts slots of item_rows rows.
+struct TreeArgs : DecodeArgs {
     TreeBatch tree;
     const uint32_t *masks;       // [total_tokens, mask_words] ancestor bits, or null (a chain)
     __nv_bfloat16 *o_lat;        // [total_tokens, H, d_c]
@@ -460,7 +463,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                        const __grid_constant__ CUtensorMap map_ckv64,
                        const __grid_constant__ CUtensorMap map_kr32,
                        const __grid_constant__ CUtensorMap map_sc,
-                       const __grid_constant__ CUtensorMap map_q, const DecodeArgs args) {
+                       const __grid_constant__ CUtensorMap map_q,
+                       const std::conditional_t<kTree, TreeArgs, DecodeArgs> args) {
     using namespace pair;
     using Walker = std::conditional_t<kTree, TreeWalker, SegmentWalker>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -720,7 +724,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                     }
                 }
             }
-            if (kTree && qk && rank == 0) args.shared[part] = shared;
+            if constexpr (kTree) {
+                if (qk && rank == 0) args.shared[part] = shared;
+            }
             if (bad_page) record_error(kErrDeviceBounds);
             // drain: the leader waits until every issued slot has landed
             // (E4M3: each CTA waits for its own code copies)
@@ -919,7 +925,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                 if (j0 < 4) {
 #pragma unroll
                     for (int i = 0; i < NSM; ++i) {
-                        const int idx = st_tid + 128 * (i + NSM * (j0 / BL));
+                        const int idx = st_tid + 128 * (i + NSM * (j0 >> (BL - 1)));
                         const int r = idx / ((NB - QT) * 8);
                         const int cc = idx - r * ((NB - QT) * 8);   // 16-byte chunk among blocks 5..8
                         const int gr = ROWS_CTA * static_cast<int>(rank) + r;
@@ -929,7 +935,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                     }
 #pragma unroll
                     for (int i = 0; i < NSM; ++i) {
-                        const int idx = st_tid + 128 * (i + NSM * (j0 / BL));
+                        const int idx = st_tid + 128 * (i + NSM * (j0 >> (BL - 1)));
                         const int r = idx / ((NB - QT) * 8);
                         const int cc = idx - r * ((NB - QT) * 8);
                         st_shared_v4(base + OFF_Q + (cc >> 3) * (ROWS_CTA * 128) + sw128(r, cc & 7), sv[i].x,
@@ -1029,35 +1035,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
             const uint32_t stg = base + OFF_EPI + static_cast<uint32_t>(warp - kSegWarp0) * 1024u;
             const int rr = lane >> 1, rc = lane & 1;   // read-back: rows rr + 16i, chunk rc
             if (kTree && slot < 0) {
-                // the whole item: O / l is final, rounded to bf16 and stored (16 columns
-                // a piece through the same staging tile)
+                if constexpr (kTree) {
+                    // the whole item: O / l is final, rounded to bf16 and stored (16 columns
+                    // a piece through the same staging tile)
 #pragma unroll 1
-                for (int cch = 0; cch < 8; ++cch) {
-                    uint32_t o[32];
-                    ptx::tmem_ld32(tmem + lane_base + TMEM_O + 32 * cch, o);
-                    ptx::tmem_wait_ld();
-                    const int ch = 256 * (cch >> 2) + 128 * half + 32 * (cch & 3);
+                    for (int cch = 0; cch < 8; ++cch) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32(tmem + lane_base + TMEM_O + 32 * cch, o);
+                        ptx::tmem_wait_ld();
+                        const int ch = 256 * (cch >> 2) + 128 * half + 32 * (cch & 3);
 #pragma unroll
-                    for (int pc = 0; pc < 2; ++pc) {
-                        uint32_t h[8];
+                        for (int pc = 0; pc < 2; ++pc) {
+                            uint32_t h[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            h[j] = pack_bf16x2(__uint_as_float(o[16 * pc + 2 * j]) * inv,
-                                               __uint_as_float(o[16 * pc + 2 * j + 1]) * inv);
-                        __syncwarp();   // the previous piece has been read back
+                            for (int j = 0; j < 8; ++j)
+                                h[j] = pack_bf16x2(__uint_as_float(o[16 * pc + 2 * j]) * inv,
+                                                   __uint_as_float(o[16 * pc + 2 * j + 1]) * inv);
+                            __syncwarp();   // the previous piece has been read back
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            st_shared_v4(stg + lane * 32 + ((c ^ ((lane >> 2) & 1)) << 4), h[4 * c], h[4 * c + 1],
-                                         h[4 * c + 2], h[4 * c + 3]);
-                        __syncwarp();
+                            for (int c = 0; c < 2; ++c)
+                                st_shared_v4(stg + lane * 32 + ((c ^ ((lane >> 2) & 1)) << 4), h[4 * c], h[4 * c + 1],
+                                             h[4 * c + 2], h[4 * c + 3]);
+                            __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int r = rr + 16 * i;
-                            const int grow_r = ROWS_CTA * static_cast<int>(rank) + ((q4 * 32 + r) & 63);
-                            const uint4 v = ld_shared_v4(stg + r * 32 + ((rc ^ ((r >> 2) & 1)) << 4));
-                            if (grow_r < rows)
-                                *reinterpret_cast<uint4 *>(args.o_lat + (out_row0 + grow_r) * DC + ch + 16 * pc +
-                                                           8 * rc) = v;
+                            for (int i = 0; i < 2; ++i) {
+                                const int r = rr + 16 * i;
+                                const int grow_r = ROWS_CTA * static_cast<int>(rank) + ((q4 * 32 + r) & 63);
+                                const uint4 v = ld_shared_v4(stg + r * 32 + ((rc ^ ((r >> 2) & 1)) << 4));
+                                if (grow_r < rows)
+                                    *reinterpret_cast<uint4 *>(args.o_lat + (out_row0 + grow_r) * DC + ch + 16 * pc +
+                                                               8 * rc) = v;
+                            }
                         }
                     }
                 }
@@ -1099,7 +1107,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                 // (kTree: a NaN sum stays NaN, so that the merge of a shared item keeps it)
                 const float lse = (kTree ? l_row != 0.f : l_row > 0.f) ? m_run * args.scale + logf(l_row) : -INFINITY;
                 if (!kTree || slot >= 0) args.lse_part[slot * (kTree ? TREE_ROWS : args.rows) + grow] = lse;
-                else if (args.lse_out) args.lse_out[out_row0 + grow] = lse;
+                if constexpr (kTree) {
+                    if (slot < 0 && args.lse_out) args.lse_out[out_row0 + grow] = lse;
+                }
             }
             ptx::tc_fence_before();
             arrive_leader(&misc->o_free);
@@ -1152,8 +1162,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kPairThreadsF
                 const int32_t tile = static_cast<int32_t>(tile_at(walk, t));
                 const int32_t tok0 = tile * TOK + half * OWN;
                 uint32_t bits = 0;   // kTree: which of the 32 tokens this row sees, read before the scores land
-                if (kTree && real_row)
-                    bits = tok0 + 32 <= vis ? ~0u : tree_bits(mask, args.mask_words, node, nodes, tok0 - vis);
+                if constexpr (kTree) {
+                    if (real_row)
+                        bits = tok0 + 32 <= vis ? ~0u : tree_bits(mask, args.mask_words, node, nodes, tok0 - vis);
+                }
                 if (!wait_bounded<false>(bar(&misc->s_full[sb]), (k / NSB) & 1, abort_flag,
                                          args.timeout_ns)) {
                     ok = false;

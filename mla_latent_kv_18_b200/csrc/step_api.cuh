@@ -145,7 +145,7 @@ mla_status decode_tree(const mla_dims *dims, const void *q, int32_t num_tokens, 
     if ((st = step_ready()) != MLA_OK) return st;
 
     const int64_t slots = 2 * static_cast<int64_t>(num_parts);
-    mla::DecodeArgs a = {};
+    mla::TreeArgs a = {};
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.block_table = block_table;
     a.seq_lens = seq_lens;

@@ -69,7 +69,7 @@ static_assert(sizeof(Misc) <= MISC_BYTES && SMEM_BYTES <= 232448, "misc");
 template <bool kSplit>
 __global__ void __launch_bounds__(tsingle::THREADS, 1)
     tree_single_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_constant__ CUtensorMap map_kr,
-                       const DecodeArgs args) {
+                       const TreeArgs args) {
     using namespace tsingle;
     constexpr int ITEM_ROWS = kSplit ? ROWS / 2 : ROWS;
     extern __shared__ uint8_t smem_raw[];
