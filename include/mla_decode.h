@@ -413,9 +413,10 @@ mla_status mla_append_kv(const mla_dims *dims, const void *ckv_new, const void *
  * with one fp32 scale per cached token, and keeps k_R in bf16:
  *   codes pool [pages, 64, d_latent] uint8 (mla_pool strides in bytes, base
  *   and strides multiples of 16), scales [pages, 64] fp32 (dense).
- * Quantisation of a row x (IEEE fp32 throughout):
+ * Quantisation of a row x (IEEE fp32 throughout, subnormal numbers as zero):
  *   amax = max |x|;  inv = 448 / amax;  code = E4M3_rn_satfinite(x * inv);
- *   scale = amax / 448          (an all-zero row: codes 0, scale 1)
+ *   scale = amax / 448          (an all-zero row, and one with amax < 448 * 2^-126,
+ *                                whose scale would be subnormal: codes 0, scale 1)
  * Dequantisation: bf16_rn( fp32_rn( value(code) * scale ) ).
  * ------------------------------------------------------------------------ */
 

@@ -869,7 +869,10 @@ struct AppendArgs {
 
 // E4M3 with one fp32 scale per token: amax over the row, then
 // inv = 448 / amax, code = E4M3_rn_satfinite(x * inv), scale = amax / 448,
-// all with IEEE-rounded fp32 operations.
+// all with IEEE-rounded fp32 operations on normal numbers; subnormal ones count as
+// zero (the build flushes them). A row with amax below kE4m3Tiny, whose scale would
+// be subnormal and whose inv could be infinite, is a zero row: codes 0, scale 1.
+constexpr float kE4m3Tiny = 448.f * 1.17549435e-38f;   // 448 * 2^-126
 __device__ __forceinline__ float amax_of8(const uint4 &v) {
     const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
     float amax = 0.f;
@@ -900,21 +903,21 @@ __device__ __forceinline__ float quantise_row_e4m3(const uint4 *src, int32_t d_c
     for (int i = lane; i < d_c / 8; i += 32) amax = fmaxf(amax, amax_of8(src[i]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 1.f;
+    const float inv = amax >= kE4m3Tiny ? __fdiv_rn(448.f, amax) : 1.f;
     for (int i = lane; i < d_c / 8; i += 32) *reinterpret_cast<uint2 *>(dst8 + 8 * i) = quantise8_e4m3(src[i], inv);
-    return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    return amax >= kE4m3Tiny ? __fdiv_rn(amax, 448.f) : 1.f;
 }
 // The same of a row of at most 512 in registers: lane holds 16-byte pieces lane and lane + 32.
 __device__ __forceinline__ float quantise_row_e4m3(const uint4 (&v)[2], int32_t d_c, uint8_t *dst8, int lane) {
     float amax = fmaxf(amax_of8(v[0]), amax_of8(v[1]));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float inv = amax > 0.f ? __fdiv_rn(448.f, amax) : 1.f;
+    const float inv = amax >= kE4m3Tiny ? __fdiv_rn(448.f, amax) : 1.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         if (lane + 32 * i < d_c / 8)
             *reinterpret_cast<uint2 *>(dst8 + 8 * (lane + 32 * i)) = quantise8_e4m3(v[i], inv);
-    return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    return amax >= kE4m3Tiny ? __fdiv_rn(amax, 448.f) : 1.f;
 }
 
 __global__ void __launch_bounds__(256) append_kv_kernel(const AppendArgs a) {

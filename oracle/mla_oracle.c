@@ -31,6 +31,7 @@
  *    seq_len beyond the table, seq_len < n_q), in which case outputs are
  *    unspecified.
  */
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
@@ -550,8 +551,9 @@ static uint16_t f32_to_bf16_rne(float f) {
 /*
  * Quantisation of rows x[r][0..d) (bf16 bits) to E4M3 with one scale per row,
  * all in IEEE fp32 (the arithmetic the kernels use, so codes agree bit for bit):
- *   amax = max |x|;  inv = 448 / amax  and  scale = amax / 448  (1 and 1 if amax = 0)
- *   code[j] = E4M3(x[j] * inv)
+ *   amax = max |x|;  inv = 448 / amax  and  scale = amax / 448  (1 and 1 if amax < 448 * 2^-126:
+ *   the scale would be subnormal)
+ *   code[j] = E4M3(x[j] * inv), with subnormal x[j] and products as zeros of their sign
  */
 void oracle_quantize_fp8_rows(int64_t R, int d, const uint16_t *x, uint8_t *codes, float *scales) {
     for (int64_t r = 0; r < R; ++r) {
@@ -562,10 +564,12 @@ void oracle_quantize_fp8_rows(int64_t R, int d, const uint16_t *x, uint8_t *code
             if (v > amax) amax = v;
         }
         volatile float num = 448.0f;
-        const float inv = amax > 0.0f ? num / amax : 1.0f;
-        scales[r] = amax > 0.0f ? amax / num : 1.0f;
+        const int zero = amax < 448.0f * FLT_MIN;
+        const float inv = zero ? 1.0f : num / amax;
+        scales[r] = zero ? 1.0f : amax / num;
         for (int j = 0; j < d; ++j) {
-            volatile float y = (float)bf16_to_f64(xr[j]) * inv;
+            const float x0 = (float)bf16_to_f64(xr[j]);
+            volatile float y = fabsf(x0) < FLT_MIN ? copysignf(0.0f, x0) : x0 * inv;
             codes[r * d + j] = oracle_e4m3_encode(y);
         }
     }

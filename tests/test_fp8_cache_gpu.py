@@ -168,3 +168,47 @@ def test_dequantising_gather_full_size_sampled(api):
     c, s = oracle.quantize_fp8_rows(rows)
     want = oracle.bf16_from_bits(oracle.dequant_fp8_rows(c, s))
     assert torch.equal(out[b.cuda(), t.cuda()].cpu(), want)
+
+
+def _near_zero_rows(d_c):
+    """Rows whose largest element is around the smallest normal fp32 numbers, and between them and ordinary ones."""
+    g = torch.Generator().manual_seed(d_c)
+    tops = [0.0, 1e-40, 1e-39, 2.0 ** -126, 1e-37, 1e-36, 1.4e-36, 5e-36, 448 * 2.0 ** -126, 6e-36, 1e-35, 1e-33, 1e-30,
+            1e-20, 1.0]
+    rows = torch.rand(2 * len(tops), d_c, generator=g, dtype=torch.float64) * 2 - 1
+    rows[:len(tops)] = 0              # one element and zeros
+    rows[:, d_c // 3] = -1
+    return (rows * torch.tensor(tops * 2, dtype=torch.float64)[:, None]).float().bfloat16()
+
+
+@pytest.mark.parametrize("by_slots,d_c", [(False, 512), (True, 512), (True, 64), (True, 576)])
+def test_append_fp8_rows_near_zero(api, by_slots, d_c):
+    """No row becomes NaN or infinite: one whose scale would be subnormal is a zero row, and fp32 subnormals are
+    zeros (the oracle's reading, bit for bit)."""
+    x = _near_zero_rows(d_c)
+    T, pages = x.shape[0], 1
+    dims = api.make_dims(1, 1, 128, d_c, 64, 128)
+    codes, scales = api.alloc_fp8_cache(pages, d_c, "cuda")
+    kr = torch.zeros(pages, 64, 64, dtype=torch.bfloat16, device="cuda")
+    kr_new = torch.zeros(T, 64, dtype=torch.bfloat16, device="cuda")
+    at = torch.arange(T, device="cuda")
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    if by_slots:
+        api.append_kv_slots_fp8(x.cuda(), kr_new, at, codes, scales, kr, dims)
+    else:
+        api.append_kv_fp8(x.cuda(), kr_new, torch.zeros_like(at).int(), at.int(), codes, scales, kr, table, dims, theta=0.0)
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+    back = api.gather_dequant_fp8(codes, scales, table, lens, T) if d_c <= 512 else None
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 0
+    want_codes, want_scales = oracle.quantize_fp8_rows(x)
+    assert np.array_equal(codes[0, :T].cpu().numpy(), want_codes)
+    assert np.array_equal(scales[0, :T].cpu().numpy(), want_scales)
+    if back is not None:
+        # half a code's step (2^-4 of the value, or 2^-10 of the scale among the subnormal codes), the two roundings
+        # of x * inv (2^-24 each), the bf16 one, and what counts as zero: fp32 subnormals, or the whole row
+        v, s = x.double(), torch.from_numpy(want_scales).double()[:, None]
+        zero = (v.abs().amax(-1, keepdim=True) < 448 * 2.0 ** -126).double() * 448 * 2.0 ** -126
+        off = (2.0 ** -4 + 2.0 ** -22) * v.abs() + 2.0 ** -10 * s * (v != 0) + 2.0 ** -126
+        bound = torch.where(zero > 0, zero, off + 2.0 ** -8 * (v.abs() + off))
+        assert ((back[0].cpu().double() - v).abs() <= bound).all()

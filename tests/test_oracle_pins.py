@@ -712,3 +712,23 @@ def test_fp8_dequant_with_power_of_two_scale_is_exact():
     prod = torch.from_numpy(codes).view(torch.float8_e4m3fn).float() * torch.from_numpy(scales)[:, None]
     lib = prod.to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
     np.testing.assert_array_equal(got, lib)
+
+
+def test_fp8_rows_near_zero():
+    """A row whose scale would be subnormal is a zero row, subnormal elements are zeros, and nothing is NaN."""
+    tiny = 2.0 ** -126
+    x = np.zeros((6, 16))
+    x[0, 3], x[0, 5] = 1e-37, -1e-37            # 448 / amax is infinite in fp32
+    x[1, :] = -5e-36                            # finite, but the scale is subnormal
+    x[2, 0], x[2, 1], x[2, 2] = 448 * tiny, -tiny, tiny / 2
+    x[3, 0], x[3, 1] = 1e-33, -2.0 ** -127
+    x[4, :] = 2.0 ** -130
+    codes, scales = oracle.quantize_fp8_rows(_bf16(x))
+    xd = _f64(_bf16(x))
+    for r in (0, 1, 4, 5):
+        assert scales[r] == 1.0 and not (codes[r] & 0x7F).any()
+    assert scales[2] == np.float32(tiny)
+    assert [oracle.e4m3_value(c) for c in codes[2, :4]] == [448.0, -1.0, 0.0, 0.0]
+    assert codes[3, 0] == 0x7E and codes[3, 1] == 0x80 and not codes[3, 2:].any()
+    back = _f64(oracle.bf16_from_bits(oracle.dequant_fp8_rows(codes, scales)))
+    assert np.isfinite(back).all() and np.abs(back - xd).max() <= 1e-33 * 2.0 ** -4 + 448 * tiny
