@@ -59,8 +59,9 @@ extern "C" {
  * A request whose lengths are negative or do not fit its table row is planned with
  * no new tokens; a token without a page (the free list ran out, or a negative old
  * table entry) gets slot -1, a table entry without one -1; a parent that does not
- * come before its child counts as none; tokens beyond num_tokens are not written,
- * and mask bits beyond max_nodes are dropped. All of these set
+ * come before its child counts as none; tokens beyond num_tokens are not written;
+ * of a request with more than max_nodes tokens, mask bits beyond max_nodes are
+ * dropped and depths end at MLA_TREE_MAX_NODES. All of these set
  * MLA_ERR_DEVICE_BOUNDS.
  * batch <= MLA_STEP_MAX_BATCH (else MLA_ERR_UNSUPPORTED). Outputs must not
  * overlap inputs; in particular free_head_out and free_head are different words.

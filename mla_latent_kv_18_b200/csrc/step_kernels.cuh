@@ -43,6 +43,7 @@ struct StepPlanArgs {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxBatch = 16384;     // two int32 sums per sequence in shared memory
 constexpr int kPlanMaxWords = 8;         // 256 tree nodes
+constexpr int kPlanMaxDepth = 32 * kPlanMaxWords;   // ancestors that a walk counts
 
 __host__ __device__ constexpr uint32_t plan_smem_bytes(int32_t batch) { return (batch + 1) * 8u; }
 
@@ -149,11 +150,11 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
             int32_t depth = i;
             if (a.parents) {
                 // up the tree; a parent comes before its child, so this ends. An entry
-                // that does not is taken for a root.
+                // that does not is taken for a root, and a request with more tokens than
+                // any tree (reported) may hold chains without a bound: their walks end early.
                 const int32_t *par = a.parents + cu[id];
-                if (i >= a.max_nodes) bad = true;
                 depth = 0;
-                for (int32_t j = i;;) {
+                for (int32_t j = i; depth < kPlanMaxDepth;) {
 #pragma unroll
                     for (int w = 0; w < kPlanMaxWords; ++w) mask[w] |= (j >> 5) == w ? 1u << (j & 31) : 0u;
                     const int32_t up = par[j];
@@ -161,6 +162,13 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
                     if (up < 0 || up >= j) break;
                     j = up;
                     ++depth;
+                }
+                if (i >= a.max_nodes) {
+                    bad = true;
+#pragma unroll
+                    for (int w = 0; w < kPlanMaxWords; ++w)
+                        if (32 * w + 31 >= a.max_nodes)
+                            mask[w] &= 32 * w >= a.max_nodes ? 0u : (1u << (a.max_nodes & 31)) - 1u;
                 }
             }
             pos = static_cast<int32_t>(c + depth);

@@ -421,3 +421,39 @@ def test_steps_together(api, fp8):
                 history[b] = [(c[i], k[i]) for i in range(n)]
             at += n
         head.copy_(plan.free_head if turn == 0 else head)
+
+
+@pytest.mark.parametrize("nodes", [1, 8, 31, 32, 33, 100, 200])
+def test_plan_masks_hold_max_nodes_bits(api, nodes):
+    """A request with more tokens than max_nodes: reported, and no bit beyond max_nodes in any mask."""
+    g = torch.Generator().manual_seed(nodes)
+    n = [nodes, nodes + 20, 3]
+    par = [[int(torch.randint(-1, i, (1,), generator=g)) if i else -1 for i in range(k)] for k in (n[0], n[1], min(3, nodes))]
+    par[2] += [-1] * (3 - len(par[2]))
+    par[1][nodes:] = range(nodes - 1, nodes + 19)      # a chain across the border
+    T = sum(n)
+    p = api.step_plan(_i32([5, 0, 60]), _i32(n), _i32(list(range(10, 40))), _i32([0]),
+                      torch.full((3, 8), 3, dtype=torch.int32, device="cuda"), T, parents=_i32(sum(par, [])), max_nodes=nodes)
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 4
+    at = 0
+    for c, k, q in zip((5, 0, 60), n, par):
+        seen = ref.ancestors(q)
+        want = torch.zeros(k, nodes, dtype=torch.bool)
+        want[:, :min(k, nodes)] = seen[:, :nodes]
+        assert torch.equal(p.masks[at:at + k].cpu(), ref.pack(want, nodes))
+        assert p.positions[at:at + k].tolist() == (c + seen.sum(1) - 1).tolist()
+        at += k
+
+
+def test_plan_walks_end(api):
+    """A chain far longer than any tree: the walk up ends after TREE_MAX_NODES ancestors, and the call reports it."""
+    n = 3000
+    p = api.step_plan(_i32([100]), _i32([n]), _i32(list(range(60))), _i32([0]),
+                      torch.full((1, 60), 3, dtype=torch.int32, device="cuda"), n, parents=_i32(list(range(-1, n - 1))),
+                      max_nodes=8)
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 4
+    assert p.positions.tolist() == [100 + min(i, api.TREE_MAX_NODES) for i in range(n)]
+    for i in (0, 3, 7, 8, 255):
+        assert p.masks[i, 0].item() == (1 << min(i + 1, 8)) - 1
