@@ -389,3 +389,71 @@ def test_tree_captured_replayed_and_on_two_streams(api):
         assert torch.equal(x[0], want_a[0]) and torch.equal(y[0], want_b[0])
         assert torch.equal(x[1], want_a[1]) and torch.equal(y[1], want_b[1])
     assert api.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dc,heads,fp8", [(512, 16, False), (512, 128, False), (64, 32, False), (512, 24, True)])
+def test_tree_attend(api, dc, heads, fp8):
+    """Both projections around the tree decode against fp64, in a padded step with a sequence that is skipped:
+    rows that no sequence owns are 0 and -inf, whatever the memory held before."""
+    s = Step(api, heads=heads, counts=[5, 4, 0, 9], lens=[300, 90, 64, 1100], dc=dc, pad=6, fp8=fp8, seed=heads)
+    g = torch.Generator("cuda").manual_seed(7)
+    dn, dv = (128 if dc == 512 else 120), 128
+    q_c, q_r = _bf16(g, s.T, heads, dn), _bf16(g, s.T, heads, s.dr)
+    q_c[-6:] = float("nan")           # rows behind the last sequence hold anything
+    w_uk, w_uv = _bf16(g, heads, dn, dc, std=dc ** -0.5), _bf16(g, heads, dc, dv, std=dc ** -0.5)
+    s.seq_lens[1] = -1                # does not fit: skipped
+    masks, ws = s.masks(), api.alloc_tree_workspace(s.dims, "cuda")
+    for shape, dtype in (((s.T, heads, dc), torch.bfloat16), ((s.T, heads), torch.float32)):
+        junk = [torch.full(shape, float("nan"), dtype=dtype, device="cuda") for _ in range(6)]
+        del junk                      # what freshly allocated outputs may hold
+    out, lse = api.tree_attend(q_c, q_r, s.codes if fp8 else s.ckv, s.kr, s.block_table, s.seq_lens, s.cu, w_uk, w_uv,
+                               s.max_nodes, masks=masks, scales=s.scales if fp8 else None, workspace=ws)
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 4
+    assert out.shape == (s.T, heads, dv) and lse.shape == (s.T, heads)
+    for rows in (slice(5, 9), slice(s.T - 6, s.T)):
+        assert (out[rows] == 0).all() and (lse[rows] == -math.inf).all()
+    for b in (0, 3):
+        L, n, at = s.lens[b], s.counts[b], sum(s.counts[:b])
+        pages = s.block_table[b, :(L + PAGE - 1) // PAGE].long()
+        c, k = s.ckv[pages].flatten(0, 1)[:L], s.kr[pages].flatten(0, 1)[:L]
+        q = torch.cat([torch.einsum("thd,hdc->thc", q_c[at:at + n].double(), w_uk.double()), q_r[at:at + n].double()], -1)
+        seen = torch.cat([torch.ones(n, L - n, dtype=torch.bool), s.seen[b]], 1)
+        o, l, A, size = tree_attention(q, c, k, s.scale, seen)
+        w = w_uv.double()
+        y = torch.einsum("thc,hcd->thd", o, w)
+        # the absorbed query is rounded to bf16 (2^-8 of each value, so at most that of the sum of a score's
+        # terms' magnitudes; 2^-9 more covers the fp32 sums): a weight is off by twice that; the weights, the
+        # latent result and the output are rounded to bf16 as well
+        ds = (2.0 ** -8 + 2.0 ** -9) * size
+        bound = torch.einsum("thc,hcd->thd", (2 * ds[..., None] + 3 * 2.0 ** -8) * A, w.abs()) + 2.0 ** -8 * y.abs()
+        got = out[at:at + n].double()
+        assert ((got - y).abs() <= bound).all()
+        assert ((lse[at:at + n].double() - l).abs() <= ds + 1e-4).all()
+        assert (got - y).norm() / y.norm() <= 0.02     # independent roundings add as squares
+
+
+@pytest.mark.parametrize("dc", [512, 64])
+def test_tree_attend_into_given_outputs(api, dc):
+    """The same bits as in outputs of its own; rows that no sequence owns keep what the buffers held, and the
+    projection is made from it."""
+    s = Step(api, heads=16, counts=[7, 2], lens=[400, 33], dc=dc, pad=3)
+    g = torch.Generator("cuda").manual_seed(1)
+    dn = 128 if dc == 512 else 120
+    args = (_bf16(g, s.T, 16, dn), _bf16(g, s.T, 16, s.dr), s.ckv, s.kr, s.block_table, s.seq_lens, s.cu,
+            _bf16(g, 16, dn, dc, std=dc ** -0.5), _bf16(g, 16, dc, 128, std=dc ** -0.5), s.max_nodes)
+    masks = s.masks()
+    want, want_lse = api.tree_attend(*args, masks=masks)
+    o = torch.ones(s.T, 16, dc, dtype=torch.bfloat16, device="cuda")
+    lse, out = torch.full((s.T, 16), 5.0, device="cuda"), torch.empty(s.T, 16, 128, dtype=torch.bfloat16, device="cuda")
+    got, got_lse = api.tree_attend(*args, masks=masks, o_lat=o, lse_out=lse, out=out)
+    assert got is out and got_lse is lse
+    assert torch.equal(out[:-3], want[:-3]) and torch.equal(lse[:-3], want_lse[:-3])
+    assert (o[-3:] == 1).all() and (lse[-3:] == 5).all() and (out[-3:] != 0).any()
+    o.zero_()
+    assert api.tree_attend(*args, masks=masks, o_lat=o, lse_out=lse, out=out)[0] is out and torch.equal(out, want)
+    for bad in (dict(out=out[:-1]), dict(out=out.float()), dict(o_lat=o[:-1]), dict(lse_out=lse.double())):
+        with pytest.raises(RuntimeError, match="MLA_ERR_INVALID_ARG"):
+            api.tree_attend(*args, masks=masks, **bad)
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 0
