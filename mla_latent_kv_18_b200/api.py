@@ -27,7 +27,6 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _binding as _b
-from . import _step
 
 _NUM_SMS = {}
 
@@ -484,7 +483,24 @@ def attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, w_uk, w_uv, scale
 TREE_MAX_NODES = 256
 STEP_MAX_BATCH = 16384
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
-_step.types(_b.MLAError, _b.MLADims)
+
+
+class _Missing:
+    """In place of a compiled binding that does not load: the calls that need it say so, all others run."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the binding of the packed-step calls (_step.so) does not load: {self.why} (run python -m "
+                          "mla_latent_kv_18_b200.build)")
+
+
+try:
+    from . import _step
+    _step.types(_b.MLAError, _b.MLADims)
+except ImportError as e:   # not built, or built for another torch or Python
+    _step = _Missing(e)
 
 
 def _on(stream, tensor):

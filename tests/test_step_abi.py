@@ -2,6 +2,9 @@
 anything is launched, sizing helpers and the rotary frequencies."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -262,3 +265,29 @@ def test_tree_attend_refuses_cpu_tensors(api, b):
 
 def test_rotary_tensor_struct_matches_the_header(b):
     assert ctypes.sizeof(b.MLARotaryTensor) == 56
+
+
+def test_the_other_calls_run_without_the_compiled_binding(b):
+    """A library without its binding of the packed-step calls: they fail loudly, decode and prefill are there."""
+    code = """
+import sys
+sys.modules['mla_latent_kv_18_b200._step'] = None    # an import of it fails
+import torch
+from mla_latent_kv_18_b200 import api
+d = api.make_dims(16, 1, 128, 512, 64, 128)
+assert api.workspace_bytes(d, 2, 4) > 0 and api.route(1, 16) == "absorb" and api._b.lib.mla_tree_num_parts(d, 148) == 74
+assert api.rope_frequencies(8)[1] == 1.0
+z = torch.zeros(2, 2, 8)
+calls = (lambda: api.step_plan(z, z, z, z, z, 8), lambda: api.rotary(z, z, z),
+         lambda: api.append_kv_slots(z, z, z, z, z, d), lambda: api.append_kv_slots_fp8(z, z, z, z, z, z, d),
+         lambda: api.decode_tree(z, z, z, z, z, z, d, 8), lambda: api.decode_tree_fp8(z, z, z, z, z, z, z, d, 8))
+for call in calls:
+    try:
+        call()
+    except ImportError as e:
+        assert "_step.so" in str(e) and "mla_latent_kv_18_b200.build" in str(e), e
+    else:
+        raise AssertionError("ran")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=300)
