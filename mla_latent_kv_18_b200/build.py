@@ -7,7 +7,9 @@ The library is a single translation unit (csrc/mla_api.cu includes every
 kernel) exporting the C ABI of include/mla_decode.h and include/mla_step.h;
 the binding (csrc/torch_step.cpp) links against it and torch.
 """
+import importlib.metadata
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -50,7 +52,7 @@ def nvcc_cmd(out=LIB, verbose=False):
 def step_cmd(out=STEP):
     import torch
     at = os.path.dirname(torch.__file__)
-    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or NVCC)))
     return [CXX, "-O2", "-std=c++17", "-shared", "-fPIC",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             "-I", INCLUDE, "-I", os.path.join(at, "include"),
@@ -61,21 +63,44 @@ def step_cmd(out=STEP):
             "-lc10_cuda"]
 
 
-def _made(out, sources, force, cmd):
-    """Make `out` with cmd(path) if it is missing or older than a source."""
+def _made_for():
+    """What _step.so depends on besides its sources: it uses the C++ interfaces of torch and Python."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:   # a torch that no installer put there
+        from torch import __version__ as version
+    return f"torch {version}, {sys.implementation.cache_tag}"
+
+
+def _made(out, sources, force, cmd, made_for=""):
+    """Make `out` with cmd(path) if it is missing, older than a source, or made for something else
+    (noted beside it)."""
+    note = out + ".for"
     if not force and os.path.exists(out):
         t = os.path.getmtime(out)
-        if all(os.path.getmtime(s) <= t for s in sources):
+        if all(os.path.getmtime(s) <= t for s in sources) and (not made_for or _read(note) == made_for):
             return
     tmp = out + ".tmp"
     subprocess.check_call(cmd(tmp))
     os.replace(tmp, out)
+    if made_for:
+        with open(note, "w") as f:
+            f.write(made_for)
+
+
+def _read(path):
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return ""
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library and the binding where they are missing or older than their sources."""
+    """Compile the library and the binding where they are missing or older than their sources, the binding
+    also where it was made for another torch or Python."""
     _made(LIB, _sources(), force, lambda out: nvcc_cmd(out, verbose))
-    _made(STEP, _step_sources(), force, step_cmd)
+    _made(STEP, _step_sources(), force, step_cmd, _made_for())
     return LIB
 
 
