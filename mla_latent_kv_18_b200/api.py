@@ -477,7 +477,8 @@ def attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, w_uk, w_uv, scale
 # a step with any number of query tokens per sequence (include/mla_step.h). The
 # calls' checks, output allocation and launches are compiled (csrc/torch_step.cpp):
 # they run on their tensors' device and its current stream, or on `stream`, a stream of
-# that device. Their outputs take no part in autograd.
+# that device. Their outputs take no part in autograd: a tensor that requires grad is written
+# with gradients off only, and the versions of the tensors that a call writes move on.
 # ----------------------------------------------------------------------------
 
 TREE_MAX_NODES = 256
@@ -677,6 +678,8 @@ def tree_attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, w
         if t.dtype != torch.bfloat16 or t.device != q_c.device or t.shape != shape or not t.is_contiguous():
             raise _b.MLAError(1, "tree_attend: contiguous bf16 q_c [T, H, d_n], q_r [T, H, d_R], w_uk [H, d_n, d_c], "
                                  "w_uv [H, d_c, d_v], out [T, H, d_v] on one device")
+    if out is not None and out.requires_grad and torch.is_grad_enabled():
+        raise _b.MLAError(1, "tree_attend: out requires grad, and autograd would not see that it is written")
     dims = make_dims(H, 1, d_n, d_c, d_r, d_v, ckv_pool.shape[1], scale)
     # decode_tree leaves rows that no sequence owns as they were, and absorb_out reads every row
     if o_lat is None:
@@ -686,4 +689,6 @@ def tree_attend(q_c, q_r, ckv_pool, kr_pool, block_table, seq_lens, cu_tokens, w
     q = absorb_q(q_c, q_r, w_uk, dims)
     _step.tree(q, ckv_pool, scales, kr_pool, block_table, seq_lens, cu_tokens, dims, max_nodes, masks, None, workspace,
                o_lat, lse_out)
+    if out is not None and not out.is_inference():
+        torch.autograd.graph.increment_version(out)
     return absorb_out(o_lat, w_uv, dims, out=out), lse_out

@@ -9,6 +9,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/CUDAContextLight.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -127,6 +128,18 @@ PyObject *wrap(const at::Tensor &t) {
     return THPVariable_Wrap(t);
 }
 
+// What a call writes is written behind autograd's back: a tensor that it tracks is refused, as torch
+// refuses a leaf in place, and the version of one that was written moves on, as after an operation of torch in
+// place, so that a backward pass which has saved it says so. (Tensors of inference mode have no version.)
+void may_write(const at::Tensor &t, const char *call, const char *name) {
+    if (t.defined() && t.requires_grad() && c10::GradMode::is_enabled())
+        throw Refused{MLA_ERR_INVALID_ARG, std::string(call) + ": " + name +
+                                               " requires grad, and autograd would not see that it is written"};
+}
+void wrote(const at::Tensor &t) {
+    if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // The tensors' device made current where it is not, and its current stream.
 struct Place {
     c10::cuda::OptionalCUDAGuard guard;
@@ -216,7 +229,11 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t) {
                             ptr<int32_t>(o[3]), ptr<int64_t>(o[4]), tree ? ptr<uint32_t>(o[6]) : nullptr,
                             ptr<int32_t>(o[5]), here.stream),
               "mla_step_plan");
-        if (!none(a[8])) return Py_NewRef(a[8]);
+        wrote(table);
+        if (!none(a[8])) {
+            for (const at::Tensor &t : o) wrote(t);
+            return Py_NewRef(a[8]);
+        }
         PyObject *r = PyTuple_New(7);
         if (!r) return nullptr;
         for (int i = 0; i < 7; ++i) PyTuple_SET_ITEM(r, i, wrap(o[i]));
@@ -253,6 +270,7 @@ PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t) {
                         t.size(2) == x.size(2) && t.size(1) <= INT32_MAX && t.sizes() == y.sizes() &&
                         ((t.stride(2) == 1 && y.stride(2) == 1) || t.size(2) == 1),
                     call, "[T, heads, width] tensors of one type, tokens and width, out of the same shape");
+            may_write(y, call, "out");
             arg[i] = {t.data_ptr(), y.data_ptr(), t.stride(0), t.stride(1), y.stride(0), y.stride(1),
                       static_cast<int32_t>(t.size(1))};
         }
@@ -264,6 +282,7 @@ PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t) {
                          static_cast<int32_t>(2 * freq.numel()), ptr<int32_t>(pos), ptr<double>(freq),
                          static_cast<float>(real(a[3], call, "mscale")), order, inverse, here.stream),
               "mla_rotary");
+        for (int i = 0; i < n; ++i) wrote(outs[i]);
         PyObject *first = none(a[7]) ? wrap(outs[0]) : Py_NewRef(a[7]);
         if (n == 1 || !first) return first;
         return Py_BuildValue("(NN)", first, none(a[9]) ? wrap(outs[1]) : Py_NewRef(a[9]));
@@ -293,8 +312,10 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t) {
         const int32_t order = layout_of(a[10], call);
         const float mscale = static_cast<float>(real(a[9], call, "mscale"));
         const Pools p = pools(a[3], a[5], d, fp8 ? at::kByte : at::kBFloat16, index, call);
+        const at::Tensor scales = flat(a[4], call, "scales", at::kFloat, index, true);
+        const at::Tensor *const cache[] = {&THPVariable_Unpack(a[3]), &THPVariable_Unpack(a[5]), &scales};
+        for (const at::Tensor *t : cache) may_write(*t, call, "the cache");
         if (fp8) {
-            const at::Tensor scales = flat(a[4], call, "scales", at::kFloat, index);
             require(scales.sizes() == at::IntArrayRef({p.pages, 64}), call, "scales [pages, 64]");
             check(mla_append_kv_slots_fp8(&d, c.data_ptr(), c.stride(0), k.data_ptr(), k.stride(0), ptr<int64_t>(slots),
                                           ptr<int32_t>(pos), ptr<double>(freq), mscale, order, static_cast<int32_t>(T),
@@ -306,6 +327,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t) {
                                       &p.ckv, &p.kr, p.pages, here.stream),
                   "mla_append_kv_slots");
         }
+        for (const at::Tensor *t : cache) wrote(*t);
         Py_RETURN_NONE;
     });
 }
@@ -355,6 +377,8 @@ PyObject *tree(PyObject *, PyObject *const *a, Py_ssize_t) {
         if (new_lse) lse = empty({T, H}, at::kFloat, index);
         require(o.sizes() == at::IntArrayRef({T, H, d.d_latent}) && lse.sizes() == at::IntArrayRef({T, H}), call,
                 "o_lat [T, H, d_c], lse_out [T, H]");
+        may_write(o, call, "o_lat");
+        may_write(lse, call, "lse_out");
         const int32_t t32 = static_cast<int32_t>(T), b32 = static_cast<int32_t>(B), n32 = static_cast<int32_t>(nodes),
                       w32 = static_cast<int32_t>(table.size(1));
         check(fp8 ? mla_decode_tree_fp8(&d, q.data_ptr(), t32, &p.ckv, ptr<float>(scales), &p.kr, p.pages,
@@ -365,6 +389,8 @@ PyObject *tree(PyObject *, PyObject *const *a, Py_ssize_t) {
                                     ptr<int32_t>(lens), ptr<int32_t>(cu), b32, ptr<uint32_t>(masks), n32, parts,
                                     ws.data_ptr(), ws.numel(), o.data_ptr(), ptr<float>(lse), here.stream),
               fp8 ? "mla_decode_tree_fp8" : "mla_decode_tree");
+        wrote(o);
+        wrote(lse);
         return Py_BuildValue("(NN)", new_o ? wrap(o) : Py_NewRef(a[12]), new_lse ? wrap(lse) : Py_NewRef(a[13]));
     });
 }

@@ -457,3 +457,81 @@ def test_plan_walks_end(api):
     assert p.positions.tolist() == [100 + min(i, api.TREE_MAX_NODES) for i in range(n)]
     for i in (0, 3, 7, 8, 255):
         assert p.masks[i, 0].item() == (1 << min(i + 1, 8)) - 1
+
+
+# ------------------------------------------------------------------ what the calls write, and autograd
+
+def _writes(api):
+    """Every call with the tensors that it writes: (name, call, written tensors)."""
+    g = torch.Generator("cuda").manual_seed(3)
+    T, H, pages = 6, 16, 3
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    dims = api.make_dims(H, 1, 128, 512, 64, 128)
+    f, m = api.rope_frequencies(64, device="cuda")
+    pos, slots = _i32(list(range(T))), torch.arange(T, device="cuda")
+    x, k, y, ky = rnd(T, H, 64), rnd(T, 2, 64), rnd(T, H, 64), rnd(T, 2, 64)
+    ckv, kr, kr8 = rnd(pages, PAGE, 512), rnd(pages, PAGE, 64), rnd(pages, PAGE, 64)
+    codes, scales = api.alloc_fp8_cache(pages, 512, "cuda")
+    c_new, k_new, q = rnd(T, 512), rnd(T, 64), rnd(T, H, 576)
+    o, lse = rnd(T, H, 512), torch.zeros(T, H, device="cuda")
+    table, plan = _i32([[0, 1]]), api.alloc_step_plan(1, T, "cuda", 8)
+    return [
+        ("plan", lambda: api.step_plan(_i32([0]), _i32([T]), _i32([2]), _i32([0]), table, T, _i32([-1] * T), 8, out=plan),
+         [table, *plan]),
+        ("rotary", lambda: api.rotary(x, pos, f, m, out=x), [x]),
+        ("rotary of two", lambda: api.rotary(x, pos, f, m, out=y, k=k, k_out=ky), [y, ky]),
+        ("append", lambda: api.append_kv_slots(c_new, k_new, slots, ckv, kr, dims, pos, f, m), [ckv, kr]),
+        ("append e4m3", lambda: api.append_kv_slots_fp8(c_new, k_new, slots, codes, scales, kr8, dims, pos, f, m),
+         [codes, scales, kr8]),
+        ("tree", lambda: api.decode_tree(q, ckv, kr, _i32([[0, 1]]), _i32([T]), _i32([0, T]), dims, 8, o_lat=o,
+                                         lse_out=lse), [o, lse]),
+    ]
+
+
+def test_versions_move_with_what_is_written(api):
+    """As after an operation of torch in place, so that autograd notices a saved tensor that has changed."""
+    for name, call, written in _writes(api):
+        before = [t._version for t in written]
+        call()
+        assert all(t._version > v for t, v in zip(written, before)), name
+    w = torch.ones(4, 2, 64, device="cuda", requires_grad=True)
+    x = torch.ones(4, 2, 64, device="cuda")
+    loss = (w * x).sum()
+    f, m = api.rope_frequencies(64, device="cuda")
+    api.rotary(x, _i32([1, 2, 3, 4]), f, m, out=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    # a refused call has written nothing
+    v = x._version
+    with pytest.raises(RuntimeError, match="MLA_ERR_INVALID_ARG"):
+        api.rotary(x, _i32([1, 2, 3, 4]), f, math.inf, out=x)
+    assert x._version == v
+    # tensors of inference mode have no version
+    with torch.inference_mode():
+        z = torch.ones(4, 2, 64, device="cuda")
+        api.rotary(z, _i32([1, 2, 3, 4]), f, m, out=z)
+    api.rotary(z, _i32([1, 2, 3, 4]), f, m, out=z)
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 0
+
+
+def test_outputs_that_require_grad_are_refused(api):
+    """Autograd does not see these writes: a tensor that it tracks is written with gradients off only."""
+    for name, call, written in _writes(api):
+        for t in written:
+            if not t.is_floating_point():
+                continue
+            t.requires_grad_(True)
+            with pytest.raises(RuntimeError, match="requires grad"):
+                call()
+            with torch.no_grad():
+                call()
+            with torch.inference_mode():
+                call()
+            t.requires_grad_(False)
+    # inputs may require one: the outputs take no part in autograd
+    f, m = api.rope_frequencies(64, device="cuda")
+    x = torch.ones(4, 2, 64, device="cuda", requires_grad=True)
+    assert not api.rotary(x, _i32([1, 2, 3, 4]), f, m).requires_grad
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 0

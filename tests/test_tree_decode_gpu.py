@@ -457,3 +457,26 @@ def test_tree_attend_into_given_outputs(api, dc):
             api.tree_attend(*args, masks=masks, **bad)
     torch.cuda.synchronize()
     assert api.get_device_error() == 0
+
+
+def test_tree_attend_and_autograd(api):
+    """The outputs that it is given, as those of the other calls: versions move, and none may require grad."""
+    s = Step(api, heads=16, counts=[3], lens=[70], dc=64)
+    g = torch.Generator("cuda").manual_seed(1)
+    args = (_bf16(g, 3, 16, 120), _bf16(g, 3, 16, 8), s.ckv, s.kr, s.block_table, s.seq_lens, s.cu,
+            _bf16(g, 16, 120, 64), _bf16(g, 16, 64, 128), s.max_nodes)
+    kw = dict(o_lat=_bf16(g, 3, 16, 64), lse_out=torch.zeros(3, 16, device="cuda"), out=_bf16(g, 3, 16, 128))
+    for t in args[-3:-1]:
+        t.requires_grad_(True)        # weights may; the result takes no part in autograd
+    before = {k: t._version for k, t in kw.items()}
+    assert not any(t.requires_grad for t in api.tree_attend(*args, **kw))
+    assert all(t._version > before[k] for k, t in kw.items())
+    for k, t in kw.items():
+        t.requires_grad_(True)
+        with pytest.raises(RuntimeError, match="requires grad"):
+            api.tree_attend(*args, **kw)
+        with torch.no_grad():
+            api.tree_attend(*args, **kw)
+        t.requires_grad_(False)
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 0
