@@ -535,3 +535,176 @@ def test_outputs_that_require_grad_are_refused(api):
     assert not api.rotary(x, _i32([1, 2, 3, 4]), f, m).requires_grad
     torch.cuda.synchronize()
     assert api.get_device_error() == 0
+
+
+# ------------------------------------------------------------------ refusals of tensors that do not fit
+
+def _fitting(api, call):
+    """Keyword arguments of a call that fits."""
+    T, H, B, pages = 7, 16, 2, 4
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    dims = api.make_dims(H, 1, 128, 512, 64, 128)
+    freq = torch.zeros(32, dtype=torch.float64, device="cuda")
+    pools = dict(ckv_pool=bf(pages, 64, 512), kr_pool=bf(pages, 64, 64), dims=dims)
+    codes = dict(ckv8_pool=torch.zeros(pages, 64, 512, dtype=torch.uint8, device="cuda"),
+                 scales=torch.zeros(pages, 64, device="cuda"), kr_pool=bf(pages, 64, 64), dims=dims)
+    if call == "step_plan":
+        return dict(cached_lens=i32(B), new_lens=i32(B), free_pages=i32(5), free_head=i32(1), block_table=i32(B, 4),
+                    num_tokens=T, parents=i32(T), max_nodes=8, out=api.alloc_step_plan(B, T, "cuda", 8))
+    if call == "rotary":
+        return dict(x=bf(T, H, 64), positions=i32(T), inv_freq=freq, out=bf(T, H, 64), k=bf(T, 2, 64), k_out=bf(T, 2, 64))
+    if call.startswith("append"):
+        return dict(ckv_new=bf(T, 512), kr_new=bf(T, 64), slots=torch.full((T,), -1, device="cuda"), positions=i32(T),
+                    inv_freq=freq, **(codes if call.endswith("fp8") else pools))
+    tree = dict(block_table=i32(B, 4), seq_lens=i32(B), cu_tokens=i32(B + 1), max_nodes=8, masks=i32(T, 1))
+    if call == "tree_attend":
+        del pools["dims"]
+        return dict(q_c=bf(T, H, 128), q_r=bf(T, H, 64), w_uk=bf(H, 128, 512), w_uv=bf(H, 512, 128), **pools, **tree)
+    return dict(q=bf(T, H, 576), workspace=api.alloc_tree_workspace(dims, "cuda"), o_lat=bf(T, H, 512),
+                lse_out=torch.zeros(T, H, device="cuda"), **tree, **(codes if call.endswith("fp8") else pools))
+
+
+def _piece(t, **kw):
+    return t._replace(**kw)
+
+
+_BF, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_WRONG = {
+    "step_plan": [
+        (dict(cached_lens=lambda t: t[:1]), r"cached_lens and new_lens \[B\]"),
+        (dict(new_lens=lambda t: t.repeat(2)), r"cached_lens and new_lens \[B\]"),
+        (dict(new_lens=lambda t: t.long()), "new_lens is a contiguous Int"),
+        (dict(cached_lens=lambda t: t.cpu()), "cached_lens is a contiguous Int"),
+        (dict(free_pages=lambda t: t.float()), "free_pages is a contiguous Int"),
+        (dict(free_head=lambda t: t.repeat(2)), "one free_head"),
+        (dict(block_table=lambda t: t.view(-1)), r"block_table \[B, max_pages\]"),
+        (dict(block_table=lambda t: t.repeat(1, 2)[:, ::2]), "block_table is a contiguous Int"),
+        (dict(block_table=lambda t: t[:, :0]), "mla_step_plan"),
+        (dict(parents=lambda t: t[:-1]), r"parents \[num_tokens\]"),
+        (dict(num_tokens=lambda t: t + 1), r"parents \[num_tokens\]"),
+        (dict(num_tokens=lambda t: -1), "num_tokens is a whole number"),
+        (dict(max_nodes=lambda t: 0), "max_nodes is a whole number"),
+        (dict(max_nodes=lambda t: 257), "max_nodes is a whole number"),
+        (dict(max_nodes=lambda t: 33), "out of other sizes"),
+        (dict(out=lambda t: t[:6]), "out is a StepPlan"),
+        (dict(out=lambda t: _piece(t, seq_lens=t.seq_lens[:1])), "out of other sizes"),
+        (dict(out=lambda t: _piece(t, cu_tokens=t.cu_tokens[:2])), "out of other sizes"),
+        (dict(out=lambda t: _piece(t, positions=t.positions[:6])), "out of other sizes"),
+        (dict(out=lambda t: _piece(t, slots=t.slots.int())), "out is a contiguous Long"),
+        (dict(out=lambda t: _piece(t, masks=t.masks.view(1, -1))), "out of other sizes"),
+        (dict(out=lambda t: _piece(t, masks=None)), "out is a tensor"),
+    ],
+    "rotary": [
+        (dict(x=lambda t: t.double()), "x is bf16, fp16 or fp32"),
+        (dict(x=lambda t: t[0]), r"x \[T, heads, width\]"),
+        (dict(positions=lambda t: t[:-1]), r"positions \[T\]"),
+        (dict(positions=lambda t: t.long()), "positions is a contiguous Int"),
+        (dict(inv_freq=lambda t: t.float()), "inv_freq is a contiguous Double"),
+        (dict(inv_freq=lambda t: t.repeat(2)), "mla_rotary"),      # 128 channels of heads of 64
+        (dict(inv_freq=lambda t: t[:0]), "mla_rotary"),
+        (dict(inv_freq=lambda t: t.view(2, 16)), r"inv_freq \[rot / 2\]"),
+        (dict(out=lambda t: t[:1]), "out of the same shape"),
+        (dict(out=lambda t: t.float()), "tensors of one type"),
+        (dict(out=lambda t: t.cpu()), "out of the same shape"),
+        (dict(out=lambda t: t[:1].expand(7, 16, 64)), "mla_rotary"),
+        (dict(k=lambda t: t[:3]), "tensors of one type, tokens and width"),
+        (dict(k=lambda t: t[..., :32]), "tensors of one type, tokens and width"),
+        (dict(k_out=lambda t: t[:, :1]), "out of the same shape"),
+        (dict(layout=lambda t: "neox"), "layout is"),
+        (dict(offset=lambda t: 2), "mla_rotary"),
+        (dict(offset=lambda t: -1), "offset is a whole number"),
+        (dict(mscale=lambda t: "one"), "mscale is a number"),
+    ],
+    "append_kv_slots": [
+        (dict(ckv_new=lambda t: t[:, :256]), r"ckv_new \[T, d_c\]"),
+        (dict(ckv_new=lambda t: t.half()), r"ckv_new \[T, d_c\]"),
+        (dict(kr_new=lambda t: t[:6]), r"kr_new \[T, d_R\]"),
+        (dict(kr_new=lambda t: t.t().contiguous().t()), r"kr_new \[T, d_R\]"),
+        (dict(kr_new=lambda t: t.cpu()), r"kr_new \[T, d_R\]"),
+        (dict(ckv_new=lambda t: t[:1].expand(7, 512)), "mla_append_kv_slots"),
+        (dict(slots=lambda t: t.int()), "slots is a contiguous Long"),
+        (dict(slots=lambda t: t[:6]), r"slots \[T\]"),
+        (dict(positions=lambda t: t[:6]), r"positions \[T\]"),
+        (dict(inv_freq=lambda t: t[:16]), r"inv_freq \[d_R / 2\]"),
+        (dict(inv_freq=lambda t: None), r"inv_freq \[d_R / 2\]"),
+        (dict(ckv_pool=lambda t: t[:, :32]), "pools"),
+        (dict(ckv_pool=lambda t: t[..., :256]), "pools"),
+        (dict(ckv_pool=lambda t: t[:3]), "pools"),
+        (dict(ckv_pool=lambda t: t.view(torch.uint8)), "pools"),
+        (dict(kr_pool=lambda t: t.transpose(1, 2)), "pools"),
+        (dict(kr_pool=lambda t: t.cpu()), "pools"),
+        (dict(ckv_pool=lambda t: t[:1].expand(4, 64, 512)), "mla_append_kv_slots"),   # pages on top of each other
+        (dict(layout=lambda t: 1), "layout is"),
+        (dict(dims=lambda t: None), "dims are make_dims'"),
+    ],
+    "append_kv_slots_fp8": [
+        (dict(scales=lambda t: t[:3]), r"scales \[pages, 64\]"),
+        (dict(scales=lambda t: t.double()), "scales is a contiguous Float"),
+        (dict(scales=lambda t: None), r"scales \[pages, 64\]"),
+        (dict(ckv8_pool=lambda t: t.view(_BF)), "pools"),
+    ],
+    "decode_tree": [
+        (dict(q=lambda t: t[..., :512].contiguous()), r"q \[T, H, d_c \+ d_R\]"),
+        (dict(q=lambda t: t[:, :8].contiguous()), r"q \[T, H, d_c \+ d_R\]"),
+        (dict(q=lambda t: t[:, :8]), "q is a contiguous BFloat16"),
+        (dict(q=lambda t: t.float()), "q is a contiguous BFloat16"),
+        (dict(q=lambda t: t.cpu()), "q is on a CUDA device"),
+        (dict(masks=lambda t: t[:-1]), r"masks \[T, ceil"),
+        (dict(masks=lambda t: t.repeat(1, 2)), r"masks \[T, ceil"),
+        (dict(max_nodes=lambda t: 33), r"masks \[T, ceil"),
+        (dict(max_nodes=lambda t: 0), "max_nodes is a whole number"),
+        (dict(max_nodes=lambda t: 257), "max_nodes is a whole number"),
+        (dict(seq_lens=lambda t: t[:1]), r"seq_lens \[B\]"),
+        (dict(seq_lens=lambda t: t.long()), "seq_lens is a contiguous Int"),
+        (dict(cu_tokens=lambda t: t[:2]), r"cu_tokens \[B \+ 1\]"),
+        (dict(block_table=lambda t: t[:1]), r"seq_lens \[B\]"),
+        (dict(block_table=lambda t: t[:, :0]), "mla_decode_tree"),
+        (dict(block_table=lambda t: t.t()), "block_table is a contiguous Int"),
+        (dict(ckv_pool=lambda t: t[:, :32]), "pools"),
+        (dict(kr_pool=lambda t: t[:3]), "pools"),
+        (dict(kr_pool=lambda t: t[..., :32]), "pools"),
+        (dict(ckv_pool=lambda t: t[:0], kr_pool=lambda t: t[:0]), "mla_decode_tree"),
+        (dict(workspace=lambda t: t[:-256]), "mla_decode_tree"),
+        (dict(workspace=lambda t: t[16:]), "mla_decode_tree"),
+        (dict(workspace=lambda t: t.view(_F32)), "workspace is a contiguous Byte"),
+        (dict(num_parts=lambda t: 1000), "mla_decode_tree"),      # more than the workspace holds
+        (dict(num_parts=lambda t: 0), "num_parts is a whole number"),
+        (dict(o_lat=lambda t: t[:6]), r"o_lat \[T, H, d_c\]"),
+        (dict(o_lat=lambda t: t.half()), "o_lat is a contiguous BFloat16"),
+        (dict(lse_out=lambda t: t[:6]), r"lse_out \[T, H\]"),
+        (dict(lse_out=lambda t: t.bfloat16()), "lse_out is a contiguous Float"),
+        (dict(dims=lambda t: 5), "dims are make_dims'"),
+    ],
+    "decode_tree_fp8": [
+        (dict(scales=lambda t: t[:3]), r"scales \[pages, 64\]"),
+        (dict(scales=lambda t: None), r"scales \[pages, 64\]"),
+        (dict(scales=lambda t: torch.zeros(257, device="cuda")[1:].view(4, 64)), "mla_decode_tree_fp8"),
+        (dict(ckv8_pool=lambda t: t[..., :256]), "pools"),
+    ],
+    "tree_attend": [
+        (dict(q_c=lambda t: t.float()), "tree_attend: contiguous bf16"),
+        (dict(q_r=lambda t: t[:6]), "tree_attend: contiguous bf16"),
+        (dict(w_uk=lambda t: t[:8]), "tree_attend: contiguous bf16"),
+        (dict(w_uv=lambda t: t.transpose(1, 2)), "tree_attend: contiguous bf16"),
+        (dict(w_uv=lambda t: t.cpu()), "tree_attend: contiguous bf16"),
+        (dict(masks=lambda t: t[:6]), r"masks \[T, ceil"),
+        (dict(ckv_pool=lambda t: t[..., :256]), "pools"),
+    ],
+}
+
+
+@pytest.mark.parametrize("call", _WRONG)
+def test_wrong_tensors_are_refused(api, call):
+    """Each argument wrong by itself, on the GPU and told by its message (the call that fits runs): sizes, types,
+    devices and strides that would otherwise become accesses out of range."""
+    from mla_latent_kv_18_b200._binding import MLAError
+    getattr(api, call)(**_fitting(api, call))
+    for change, message in _WRONG[call]:
+        kw = _fitting(api, call)
+        for name, f in change.items():
+            kw[name] = f(kw.get(name))
+        with pytest.raises(MLAError, match=message):
+            getattr(api, call)(**kw)
+    torch.cuda.synchronize()
+    assert api.get_device_error() == 0
