@@ -63,6 +63,10 @@ extern "C" {
  * of a request with more than max_nodes tokens, mask bits beyond max_nodes are
  * dropped and depths end at MLA_TREE_MAX_NODES. All of these set
  * MLA_ERR_DEVICE_BOUNDS.
+ * After a step of which not every token is kept, cached_lens[b] of the next plan ends where the
+ * kept tokens still lie one after the other (those of a tree's path that do not are written again,
+ * as new tokens). The pages past it, entries ceil(cached / 64) .. ceil(seq_len / 64) of the row, are the
+ * caller's to put back on the free list first: the next plan takes fresh ones for them.
  * batch <= MLA_STEP_MAX_BATCH (else MLA_ERR_UNSUPPORTED). Outputs must not
  * overlap inputs; in particular free_head_out and free_head are different words.
  * batch = 0 writes the padded rows, cu_tokens[0] = 0 and free_head_out.

@@ -546,7 +546,13 @@ def step_plan(cached_lens, new_lens, free_pages, free_head, block_table, num_tok
       masks [num_tokens, ceil(max_nodes / 32)]   with parents: bits of the token and its ancestors
 
     parents [num_tokens] int32: index within the request of the drafted token each token follows
-    (an earlier one; negative: it follows the context); max_nodes bounds new_lens then."""
+    (an earlier one; negative: it follows the context); max_nodes bounds new_lens then.
+
+    Pages of tokens that are not kept are the caller's to put back: entries ceil(cached / 64) ..
+    ceil(seq_len / 64) of a request's row, before the next plan overwrites them with fresh ones. Kept tokens that
+    do not lie one after the other in the cache (a tree's path) are written again, as new tokens. decode_tree
+    takes up to TREE_MAX_NODES new tokens per request, with or without parents. Without `out` the outputs
+    share one allocation."""
     if stream is not None:
         with _on(stream, block_table):
             return step_plan(cached_lens, new_lens, free_pages, free_head, block_table, num_tokens, parents, max_nodes,

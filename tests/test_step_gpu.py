@@ -708,3 +708,77 @@ def test_wrong_tensors_are_refused(api, call):
             getattr(api, call)(**kw)
     torch.cuda.synchronize()
     assert api.get_device_error() == 0
+
+
+# ------------------------------------------------------------------ drafts accepted in part
+
+def test_turns_with_drafts_accepted_in_part(api):
+    """Turns of draft trees of which a path is accepted. Accepted tokens that already lie at their places stay
+    (the request's cached length grows over them); the others of the path are written again, first in the
+    next step, as a chain before its drafts. Pages past the cached length go back to the free list before the
+    next plan, which overwrites their entries: no page is lost, and none has two owners."""
+    B, H, dc, dr, nodes, pages = 3, 16, 512, 64, 96, 21
+    g, host = torch.Generator("cuda").manual_seed(5), torch.Generator().manual_seed(5)
+    draw = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=host))  # noqa: E731
+    dims, scale = api.make_dims(H, 1, 128, dc, dr, 128), 1 / math.sqrt(192)
+    f, m = api.rope_frequencies(dr, device="cuda")
+    ckv = torch.zeros(pages, PAGE, dc, dtype=torch.bfloat16, device="cuda")
+    kr = torch.zeros(pages, PAGE, dr, dtype=torch.bfloat16, device="cuda")
+    table = torch.full((B, 7), -1, dtype=torch.int32, device="cuda")
+    free = torch.randperm(pages, generator=host).tolist()
+    history = [[] for _ in range(B)]   # accepted tokens: rows [c | k], the key not turned
+    cached, given_back, again = [0] * B, set(), 0
+    for turn in range(9):
+        pending = [h[c:] for h, c in zip(history, cached)]
+        drafts = [draw(1, 40) if turn else (50, 3, 90)[b] for b in range(B)]
+        new = [len(p) + n for p, n in zip(pending, drafts)]
+        parents, rows = [], []
+        for p, n in zip(pending, drafts):
+            chain = list(range(-1, len(p) - 1))
+            own = [len(p) + (draw(-1, i - 1) if turn else i - 1) for i in range(n)]   # len(p) - 1: follows the context
+            parents += chain + own
+            rows += p + list(torch.randn(n, dc + dr, generator=g, device="cuda").bfloat16())
+        kv = torch.stack(rows)
+        T = sum(new)
+        p = api.step_plan(_i32(cached), _i32(new), _i32(free), _i32([0]), table, T, _i32(parents), nodes + 40)
+        api.append_kv_slots(kv[:, :dc], kv[:, dc:], p.slots, ckv, kr, dims, p.positions, f, m)
+        q = torch.randn(T, H, dc + dr, generator=g, device="cuda").bfloat16()
+        o, lse = api.decode_tree(q, ckv, kr, table, p.seq_lens, p.cu_tokens, dims, nodes + 40, masks=p.masks)
+        torch.cuda.synchronize()
+        assert api.get_device_error() == 0
+        head = p.free_head.item()
+        again += len(given_back & set(free[:head]))
+        free = free[head:]
+        at = 0
+        for b, n in enumerate(new):
+            seen = ref.ancestors(parents[at:at + n])
+            old = torch.stack(history[b][:cached[b]] or [kv[0]])[:cached[b]]
+            c = torch.cat([old, kv[at:at + n]])
+            pos = torch.cat([torch.arange(cached[b]), cached[b] + seen.sum(1) - 1]).int().cuda()
+            assert p.positions[at:at + n].tolist() == pos[cached[b]:].tolist()
+            # the cached keys: the fp64 turn rounded to bf16 is within one step of the kernel's, so the reference
+            # reads them from the cache, whose turn is tested by itself, and only checks that they are these tokens'
+            where = table[b].long().repeat_interleave(PAGE)[:cached[b] + n] * PAGE + torch.arange(cached[b] + n, device="cuda") % PAGE
+            assert torch.equal(ckv.view(-1, dc)[where], c[:, :dc])
+            k = kr.view(-1, dr)[where]
+            _turn_check(k[:, None], c[:, None, dc:], pos, f, m, "interleaved", 0)
+            full = torch.cat([torch.ones(n, cached[b], dtype=torch.bool), seen], 1)
+            ref.check_tree(o[at:at + n], lse[at:at + n], ref.tree_attention(q[at:at + n], c[:, :dc], k, scale, full), len(c))
+            # accept a path (in the first turn the whole chain)
+            node = draw(len(pending[b]) - 1, n - 1) if turn else n - 1
+            path = seen[node].nonzero()[:, 0].tolist() if node >= 0 else []
+            history[b] = history[b][:cached[b]] + [kv[at + i] for i in path]
+            stay = 0
+            while stay < len(path) and path[stay] == stay:
+                stay += 1
+            end = (cached[b] + n + PAGE - 1) // PAGE
+            cached[b] += stay
+            at += n
+            back = range((cached[b] + PAGE - 1) // PAGE, end)
+            returned = [int(table[b, i]) for i in back]
+            free, given_back = returned + free, given_back | set(returned)   # the next plan takes them first
+            for i in back:
+                table[b, i] = -1
+        owned = [int(v) for v in table.view(-1) if v >= 0]
+        assert sorted(owned + free) == list(range(pages))
+    assert again > 0          # pages have come round
