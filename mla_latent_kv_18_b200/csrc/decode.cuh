@@ -24,10 +24,13 @@
 //    CTA, cta_group::1, M = 128 rows; the 8-wide RoPE key is padded to the
 //    16-wide MMA K step with a zero core-matrix column in shared memory.
 //
-// Both are templates over the work they walk (kTree): whole sequences of n_q
-// query tokens with one partial result per (sequence, partition), or the row
+// The pair kernel is a template over the work it walks (kTree): whole sequences of
+// n_q query tokens with one partial result per (sequence, partition), or the row
 // blocks of a step with any number of query tokens per sequence under an ancestor
-// mask (tree_plan.cuh), where a block that one partition covers is final.
+// mask (tree_plan.cuh), where a block that one partition covers is final. (Such
+// steps at d_c 64 have a kernel of their own, tree_single.cuh.)
+// P is rounded to bf16, the value product's operand type (half a step, 2^-8 of a
+// weight, either way); the row sums add the weights as they are, in fp32.
 //
 // Every wait is bounded (see wait_bounded); data errors set the device error
 // word. The kernels never read block-table entries past a sequence's last
@@ -261,10 +264,11 @@ constexpr uint32_t OFF_FIRST_WALKER = OFF_EPI + 64;   // kTree: the walker at it
 constexpr int TREE_ROWS = 2 * ROWS_CTA;               // kTree: query rows per item
 constexpr int TREE_MIN_TILES = 4;                     // kTree: see tree_find
 constexpr int TREE_WHOLE = 10;
-// kTree: cost of a switch in tiles, measured: 16 ragged sequences of up to 4096 tokens,
-// 4 nodes, bf16 cache 42.0 us with 8, 39.8 with 6, 44.8 with 14 (16 equal ones with 8 nodes:
-// 155.0, 155.4, 154.7); E4M3 cache, whose tiles take longer, 65.1 us with 8, 59.9 with 5,
-// 70.2 with 14 (before its rings were widened by warps of their own: 57.3 now).
+// kTree: cost of a switch in tiles. Device times in us, ragged sequences of 128 heads:
+//   bf16 with 3, 6, 10:  16 to 4096 tokens, 4 nodes: 44.5, 40.1, 43.3;  64 to 1000, 3: 66.2, 58.2, 54.0;
+//                        8 to 20000, 6: 105.8, 103.8, 102.7;  16 equal ones of 4096, 8: 155.4, 154.7, 154.8
+//   E4M3 with 3, 5, 8:   16 to 4096, 4: 57.1, 57.4, 61.3;  64 to 1000, 3: 78.3, 77.1, 78.7;
+//                        8 to 20000, 2: 84.7, 85.2, 85.5 (its tiles take longer)
 constexpr int TREE_GAP = 6, TREE_GAP_FP8 = 5;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TMEM_O = 0;                 // two 128-column accumulators (c = 0, 1)

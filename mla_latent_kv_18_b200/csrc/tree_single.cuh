@@ -11,11 +11,14 @@
 // the scores in their own buffer, as bf16 pairs, the value product's A operand: no
 // shared-memory copy of it. Three score buffers let the score products run ahead, and
 // the two products are issued by a warp each, on blocking waits.
-// Measured, 32 sequences of 8192 tokens, 32 nodes of 32 heads (110 tiles a SM): 135 us, about
-// 2100 cycles a tile, the special-function units busy half of the time and
-// the warps waiting on dependent instructions the rest. One group of four warps took 162 us, one
+// Measured, 32 sequences of 8192 tokens, 32 heads: 135 us with 32 nodes (8 items of 128 rows a sequence,
+// 111 passes over a tile per SM), 80 with 16, 64 with 12, 47 with 8 and 31 with 4 (one item, 14 passes): 1.0
+// to 1.2 us a pass, about 2100 cycles, the special-function units busy half of the time and the warps
+// waiting on dependent instructions the rest, and 14 us for start, switches and merge. An item costs its
+// pass whatever its rows: 5 nodes (160 rows) take 45 us. One group of four warps took 162 us, one
 // issuer polling for both products 146, four groups on 64-token tiles 158, two on 64-token
-// tiles 184 (more waits per score).
+// tiles 184 (more waits per score), at 32 nodes. P is rounded to bf16 (half a step, 2^-8 of a weight, either
+// way); the row sums add the weights as they are, in fp32.
 //
 // kSplit (items of at most 64 rows): query row r sits in MMA rows 32 (r / 16) + r % 16
 // and the same + 16, both TMEM lanes of one warp; the first lane takes the tile's
@@ -43,7 +46,10 @@ constexpr int THREADS = 352;                              // TMA, QK^T, 2 x 4 so
 constexpr int STAGES = 8;                                 // KV ring depth
 constexpr int NSB = 3;                                    // score buffers
 constexpr int MIN_TILES = 2, WHOLE = 4;                   // see tree_find
-constexpr int GAP = 3;                                    // cost of a switch, in tiles
+// Cost of a switch, in tiles. Device times in us with 1, 3, 6, 10, 32 heads: 32 x 8192 tokens, 5 nodes: 46.0,
+// 44.9, 44.4, 45.2; the same ragged: 28.9, 26.7, 24.7, 25.1; 64 ragged to 1000, 3 nodes: 20.8, 18.3, 19.4, 20.6;
+// 200 ragged to 600, 8 nodes: 41.2, 36.1, 34.2, 33.8.
+constexpr int GAP = 3;
 constexpr uint32_t OFF_Q = 0;
 constexpr uint32_t OFF_STAGE = 20480;
 constexpr uint32_t OFF_MISC = OFF_STAGE + STAGES * STAGE_BYTES;
